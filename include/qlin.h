@@ -39,7 +39,7 @@
  *     share a workspace.  The library keeps no state besides the thread-local
  *     error message and a per-device cache of the compute-unit count.
  *   - Workspace (qlin_w4_forward, qlin_w4_forward_perm, spqr_forward,
- *     sq_int8_gemm, qlin_f16_gemm): device
+ *     sq_int8_gemm, qlin_f16_gemm, qlin_kv8_attention): device
  *     memory of at least the size the matching *_workspace_bytes call reports
  *     for the shape (0 means none is needed and NULL may be passed), 16-byte
  *     aligned.  Fill the whole buffer with zeros once after allocating it:
@@ -324,6 +324,116 @@ qlin_status qlin_f16_gemm_workspace_bytes(int M, int N, int K, int y_dtype, size
  * in the conventions at the top. */
 qlin_status qlin_f16_gemm(const uint16_t* X, const uint16_t* W, int M, int N, int K, void* Y, int y_dtype,
                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ======================================================================== */
+/* 8-bit paged key/value cache: append, attention, gather                    */
+/* ======================================================================== */
+/* The attention between a layer's QKV and output projections, over a cache in
+ * the library's low-bit manner: int8 codes with one fp32 scale for each block
+ * of tokens and head (value = scale * code).  A sequence's tokens live in pages
+ * of page_size tokens anywhere in a pool; its block table names them in order.
+ *
+ *   k_codes int8 [num_pages][kv_heads][page_size][head_dim]
+ *   v_codes int8 [num_pages][kv_heads][head_dim][page_size]  (tokens contiguous)
+ *   scales  fp32 [num_pages][kv_heads][2]                    (K scale, V scale)
+ *
+ * Pages need no initialization: the first append into a page starts its scales.
+ * head_dim 64, 128 or 256; page_size 16, 32, 64 or 128 (EUNSUPPORTED otherwise).
+ * Offsets into the pool are 64-bit.                                           */
+typedef struct {
+  int8_t* k_codes;
+  int8_t* v_codes;
+  float* scales;
+  int num_pages, kv_heads, head_dim, page_size;
+} qlin_kv8_cache;
+
+/* A ragged batch.  Sequence b owns the call's tokens offsets[b] ..
+ * offsets[b+1]-1, the last ones of its kv_lens[b] tokens: token i of them sits
+ * at position kv_lens[b] - n_b + i.  block_table[b][p] is the page of positions
+ * p * page_size ...; one batch serves an append and the attention after it.
+ * max_new and max_kv say how much work to plan for (the longest n_b and
+ * kv_lens[b]); sequences that exceed them are still computed in full, only
+ * slower, so a captured graph may be replayed while device lengths grow.
+ * The device arrays are trusted for meaning but not for memory safety:
+ * offsets are clamped into 0 .. tokens, lengths into 0 .. table_stride *
+ * page_size, and block table entries outside 0 .. num_pages-1 (-1 marks a page
+ * given back to the pool) are never dereferenced: their tokens are not
+ * stored, and not visible.  Tokens at negative positions (n_b > kv_lens[b]) are
+ * not stored and see nothing. */
+typedef struct {
+  const int32_t* offsets;      /* device [seqs + 1] */
+  const int32_t* kv_lens;      /* device [seqs] */
+  const int32_t* block_table;  /* device [seqs][table_stride] */
+  int seqs, tokens, table_stride, max_new, max_kv;
+} qlin_kv8_batch;
+
+/* Which dimensions turn together: (i, i + rot_dim/2), or (2i, 2i + 1). */
+typedef enum { QLIN_ROPE_HALF = 0, QLIN_ROPE_PAIRS = 1 } qlin_rope_style;
+
+/* Byte sizes of a cache's three arrays.  EINVAL for sizes <= 0, EUNSUPPORTED as
+ * above. */
+qlin_status qlin_kv8_sizes(int num_pages, int kv_heads, int head_dim, int page_size,
+                           size_t* k_bytes, size_t* v_bytes, size_t* scale_bytes);
+
+/* Rotate the new queries and keys by their positions and store the new keys and
+ * values in their pages.
+ *   Q device [tokens][q_heads][head_dim], K and V [tokens][kv_heads][head_dim],
+ *     dtype QLIN_F16 or QLIN_BF16; consecutive tokens are q_stride / k_stride /
+ *     v_stride elements apart (multiples of 8, at least the heads' extent), so
+ *     the three may be slices of one fused projection
+ *   cos, sin device fp32 [max_pos][rot_dim / 2] (positions past max_pos-1 use the
+ *     last row); the first rot_dim dimensions turn: (a, b) -> (a cos - b sin,
+ *     b cos + a sin).  rot_dim a multiple of 16 up to head_dim; 0: none, tables NULL
+ *   Q_out device [tokens][q_heads][head_dim] of dtype, the rotated queries
+ *     (Q itself where q_stride = q_heads * head_dim, otherwise no overlap);
+ *     Q and Q_out both NULL: keys and values only
+ * Quantization, in fp32, per page and head, K and V apart: a = max |x| over the
+ * page's new tokens; s = a / 127, or the page's scale s_old if it already holds
+ * earlier tokens of the sequence and s_old is larger; codes
+ * clamp(rint(x * (1 / s)), -127, 127).  Where s > s_old the earlier tokens' codes
+ * become rint(q * (s_old * (1 / s))).  s below 2^-126 counts as 0, codes 0.  A
+ * NaN or infinity among the page's values makes its scale NaN (until the page
+ * is started anew): whoever sees a token of it gets NaN, nobody else does.
+ * No two sequences of a call may store into the same page.  Requirements: seqs,
+ * tokens, q_heads, max_new, max_kv > 0, q_heads a multiple of kv_heads (ignored
+ * without Q), tokens * heads * head_dim < 2^40, seqs and heads <= 65535. */
+qlin_status qlin_kv8_append(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
+                            const void* Q, const void* K, const void* V, int dtype, int q_heads,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            const float* cos, const float* sin, int max_pos, int rot_dim, int rope_style,
+                            void* Q_out, hipStream_t stream);
+
+/* The cached values of the batch's tokens (keys as rotated) back in 16 bits:
+ * K_out, V_out device [tokens][kv_heads][head_dim] of dtype QLIN_F16 or QLIN_BF16,
+ * scale * code rounded once (0 for tokens that are not stored). */
+qlin_status qlin_kv8_gather(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
+                            void* K_out, void* V_out, int dtype, hipStream_t stream);
+
+/* Device workspace bytes of qlin_kv8_attention for these sizes on the current
+ * device (0: none); only the sizes in cache and batch are read. */
+qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
+                                               int q_heads, int window, int sinks, size_t* bytes);
+
+/* Y = softmax(scale Q K^T + mask) V over the cached tokens.  The query at
+ * position p sees the cached positions j <= p with, for window > 0, j > p -
+ * window or j < sinks (a sliding window and a few first tokens that stay
+ * visible; window 0: all of them, sinks then has to be 0).  Query heads share
+ * key/value heads in runs of q_heads / kv_heads.  Queries that see nothing give
+ * zeros.
+ *   Q device, tokens q_stride elements apart (a multiple of 8), Y device
+ *   [tokens][q_heads][head_dim], both of dtype QLIN_F16 or QLIN_BF16; Y must not
+ *   overlap Q.  scale: finite, > 0.
+ *   workspace: conventions at the top.
+ * Codes enter the matrix instructions as exact fp16 integers and products are
+ * summed in fp32; bf16 queries are scaled to fp16 by a power of two per row (as
+ * in qlin_w4_forward); softmax statistics are fp32; the weights are rounded to
+ * fp16 relative to their row's running maximum.  Long sequences are
+ * split over workgroups and joined in a fixed order: results do not depend on
+ * timing. */
+qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
+                               const void* Q, int dtype, int q_heads, int64_t q_stride,
+                               float scale, int window, int sinks, void* Y,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ======================================================================== */
 /* Second-order encoders (host, offline): same storage, same forward calls   */

@@ -3,9 +3,12 @@
 // Every check happens on the host before anything is enqueued; device arrays
 // are never read here.
 
+#include <algorithm>
+#include <cmath>
 #include <string>
 
 #include "common.hpp"
+#include "kv8.hpp"
 #include "launch.hpp"
 
 using namespace qlin;
@@ -158,6 +161,93 @@ qlin_status dense_workspace_total(int M, int N, int K, int y_dtype, size_t* tota
   size_t partial = 0;
   QLIN_TRY(dense_f16_gemm_launch(nullptr, nullptr, M, N, K, nullptr, y_dtype, WsView{}, &partial, nullptr));
   *total = kCounterBytes + ws_round(partial);
+  return QLIN_OK;
+}
+
+// Sizes of a cache: head_dim and page_size are ones that the kernels exist for.
+qlin_status kv8_check_sizes(const char* fn, int pages, int heads, int dim, int page_size) {
+  if (pages <= 0 || heads <= 0 || dim <= 0 || page_size <= 0)
+    return fail(QLIN_EINVAL, std::string(fn) + ": num_pages, kv_heads, head_dim and page_size must be positive");
+  if (dim != 64 && dim != 128 && dim != 256)
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": head_dim must be 64, 128 or 256");
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": page_size must be 16, 32, 64 or 128");
+  if (heads > 32767) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": kv_heads above 32767");
+  return QLIN_OK;
+}
+
+// Checks cache and batch and makes the kernels' view of them; with sizes_only
+// the pointers may be NULL.
+qlin_status kv8_view(const char* fn, const qlin_kv8_cache* c, const qlin_kv8_batch* b, bool sizes_only, Kv8View* v) {
+  if (!c || !b) return fail(QLIN_EINVAL, std::string(fn) + ": NULL cache or batch");
+  QLIN_TRY(kv8_check_sizes(fn, c->num_pages, c->kv_heads, c->head_dim, c->page_size));
+  if (b->seqs <= 0 || b->tokens <= 0 || b->table_stride <= 0 || b->max_new <= 0 || b->max_kv <= 0)
+    return fail(QLIN_EINVAL, std::string(fn) + ": seqs, tokens, table_stride, max_new and max_kv must be positive");
+  if (b->seqs > 65535) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": more than 65535 sequences");
+  if (!sizes_only) {
+    if (!c->k_codes || !c->v_codes || !c->scales) return fail(QLIN_EINVAL, std::string(fn) + ": NULL cache pointer");
+    if (!b->offsets || !b->kv_lens || !b->block_table) return fail(QLIN_EINVAL, std::string(fn) + ": NULL batch pointer");
+    QLIN_TRY(need_aligned(fn, "k_codes", c->k_codes));
+    QLIN_TRY(need_aligned(fn, "v_codes", c->v_codes));
+    QLIN_TRY(need_aligned(fn, "scales", c->scales));
+    QLIN_TRY(need_aligned(fn, "offsets", b->offsets));
+    QLIN_TRY(need_aligned(fn, "kv_lens", b->kv_lens));
+    QLIN_TRY(need_aligned(fn, "block_table", b->block_table));
+  }
+  int log_page = 4;
+  while ((1 << log_page) < c->page_size) ++log_page;
+  // no call brings more than its tokens, and no sequence outgrows its table
+  const long long room = static_cast<long long>(b->table_stride) * c->page_size;
+  *v = Kv8View{c->k_codes, c->v_codes, c->scales, b->offsets, b->kv_lens, b->block_table,
+               c->num_pages, c->kv_heads, c->head_dim, log_page,
+               b->seqs, b->tokens, b->table_stride, std::min(b->max_new, b->tokens),
+               static_cast<int>(std::min<long long>(b->max_kv, room))};
+  return QLIN_OK;
+}
+
+qlin_status kv8_check_dtype(const char* fn, int dtype) {
+  if (dtype != QLIN_F16 && dtype != QLIN_BF16) return fail(QLIN_EINVAL, std::string(fn) + ": dtype must be F16 or BF16");
+  return QLIN_OK;
+}
+
+qlin_status kv8_check_rows(const char* fn, const char* name, int tokens, int heads, int dim, int64_t stride) {
+  const int64_t extent = static_cast<int64_t>(heads) * dim;
+  if (stride < extent || stride % 8 != 0)
+    return fail(QLIN_EINVAL, std::string(fn) + ": " + name + " must be a multiple of 8 and at least heads * head_dim");
+  if (stride > (int64_t{1} << 40) / tokens) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": " + name + " too large");
+  return QLIN_OK;
+}
+
+qlin_status kv8_check_heads(const char* fn, int q_heads, int kv_heads) {
+  if (q_heads <= 0 || q_heads % kv_heads != 0)
+    return fail(QLIN_EINVAL, std::string(fn) + ": q_heads must be a positive multiple of kv_heads");
+  if (q_heads > 65535) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": q_heads above 65535");
+  return QLIN_OK;
+}
+
+bool kv8_overlap(const void* x, int64_t x_bytes, const void* y, int64_t y_bytes) {
+  const char* p = static_cast<const char*>(x);
+  const char* q = static_cast<const char*>(y);
+  return p < q + y_bytes && q < p + x_bytes;
+}
+
+// Bytes from the first to the last value of `tokens` rows.
+int64_t kv8_span(int tokens, int heads, int dim, int64_t stride) {
+  return 2 * ((tokens - 1) * stride + static_cast<int64_t>(heads) * dim);
+}
+
+qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, int q_heads,
+                          int window, int sinks, bool sizes_only, Kv8AttnArgs* a, size_t* total) {
+  QLIN_TRY(kv8_view(fn, cache, batch, sizes_only, &a->c));
+  QLIN_TRY(kv8_check_heads(fn, q_heads, a->c.heads));
+  if (window < 0 || sinks < 0) return fail(QLIN_EINVAL, std::string(fn) + ": window and sinks must not be negative");
+  if (sinks > 0 && window == 0) return fail(QLIN_EINVAL, std::string(fn) + ": sinks without a window");
+  a->q_heads = q_heads;
+  a->group = q_heads / a->c.heads;
+  a->window = window;
+  a->sinks = sinks;
+  const size_t partial = kv8_attn_plan(a);
+  *total = partial ? kCounterBytes + ws_round(partial) : 0;
   return QLIN_OK;
 }
 
@@ -349,6 +439,126 @@ qlin_status qlin_f16_gemm(const uint16_t* X, const uint16_t* W, int M, int N, in
   QLIN_TRY(need_workspace(fn, workspace, workspace_bytes, total));
   QLIN_TRY(dense_f16_gemm_launch(X, W, M, N, K, Y, y_dtype, WsView{static_cast<char*>(workspace), workspace_bytes},
                                  nullptr, stream));
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_sizes(int num_pages, int kv_heads, int head_dim, int page_size, size_t* k_bytes, size_t* v_bytes,
+                           size_t* scale_bytes) {
+  static const char* fn = "qlin_kv8_sizes";
+  clear_error();
+  QLIN_TRY(kv8_check_sizes(fn, num_pages, kv_heads, head_dim, page_size));
+  if (!k_bytes || !v_bytes || !scale_bytes) return fail(QLIN_EINVAL, std::string(fn) + ": NULL pointer");
+  const size_t blocks = static_cast<size_t>(num_pages) * kv_heads;
+  *k_bytes = *v_bytes = blocks * page_size * head_dim;
+  *scale_bytes = blocks * 2 * sizeof(float);
+  return QLIN_OK;
+}
+
+qlin_status qlin_kv8_append(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, const void* Q, const void* K,
+                            const void* V, int dtype, int q_heads, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const float* cos, const float* sin, int max_pos, int rot_dim,
+                            int rope_style, void* Q_out, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_append";
+  clear_error();
+  Kv8AppendArgs a{};
+  QLIN_TRY(kv8_view(fn, cache, batch, false, &a.c));
+  QLIN_TRY(kv8_check_dtype(fn, dtype));
+  const int T = a.c.tokens, D = a.c.dim;
+  if (!K || !V) return fail(QLIN_EINVAL, std::string(fn) + ": NULL K or V");
+  if (!Q != !Q_out) return fail(QLIN_EINVAL, std::string(fn) + ": Q and Q_out must both be given, or neither");
+  if (rope_style != QLIN_ROPE_HALF && rope_style != QLIN_ROPE_PAIRS)
+    return fail(QLIN_EINVAL, std::string(fn) + ": rope_style must be QLIN_ROPE_HALF or QLIN_ROPE_PAIRS");
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0)
+    return fail(QLIN_EINVAL, std::string(fn) + ": rot_dim must be a multiple of 16 from 0 to head_dim");
+  if (rot_dim > 0) {
+    if (!cos || !sin || max_pos <= 0) return fail(QLIN_EINVAL, std::string(fn) + ": rotation needs cos, sin and max_pos > 0");
+    QLIN_TRY(need_aligned(fn, "cos", cos));
+    QLIN_TRY(need_aligned(fn, "sin", sin));
+  }
+  QLIN_TRY(need_aligned(fn, "K", K));
+  QLIN_TRY(need_aligned(fn, "V", V));
+  QLIN_TRY(kv8_check_rows(fn, "k_stride", T, a.c.heads, D, k_stride));
+  QLIN_TRY(kv8_check_rows(fn, "v_stride", T, a.c.heads, D, v_stride));
+  if (Q) {
+    QLIN_TRY(need_aligned(fn, "Q", Q));
+    QLIN_TRY(need_aligned(fn, "Q_out", Q_out));
+    QLIN_TRY(kv8_check_heads(fn, q_heads, a.c.heads));
+    QLIN_TRY(kv8_check_rows(fn, "q_stride", T, q_heads, D, q_stride));
+    const int64_t packed = static_cast<int64_t>(q_heads) * D, out = kv8_span(T, q_heads, D, packed);
+    if (!(Q == Q_out && q_stride == packed) && kv8_overlap(Q, kv8_span(T, q_heads, D, q_stride), Q_out, out))
+      return fail(QLIN_EINVAL, std::string(fn) + ": Q_out overlaps Q");
+    if (kv8_overlap(K, kv8_span(T, a.c.heads, D, k_stride), Q_out, out) ||
+        kv8_overlap(V, kv8_span(T, a.c.heads, D, v_stride), Q_out, out))
+      return fail(QLIN_EINVAL, std::string(fn) + ": Q_out overlaps K or V");
+  }
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.K = static_cast<const uint16_t*>(K);
+  a.V = static_cast<const uint16_t*>(V);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_heads = q_heads;
+  a.cos = cos;
+  a.sin = sin;
+  a.max_pos = max_pos;
+  a.rot = rot_dim;
+  a.pairs = rope_style == QLIN_ROPE_PAIRS;
+  a.Q_out = static_cast<uint16_t*>(Q_out);
+  kv8_append_launch(a, dtype, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_gather(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, void* K_out, void* V_out,
+                            int dtype, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_gather";
+  clear_error();
+  Kv8View c;
+  QLIN_TRY(kv8_view(fn, cache, batch, false, &c));
+  QLIN_TRY(kv8_check_dtype(fn, dtype));
+  if (!K_out || !V_out) return fail(QLIN_EINVAL, std::string(fn) + ": NULL K_out or V_out");
+  QLIN_TRY(need_aligned(fn, "K_out", K_out));
+  QLIN_TRY(need_aligned(fn, "V_out", V_out));
+  kv8_gather_launch(c, static_cast<uint16_t*>(K_out), static_cast<uint16_t*>(V_out), dtype, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, int q_heads,
+                                               int window, int sinks, size_t* bytes) {
+  static const char* fn = "qlin_kv8_attention_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(QLIN_EINVAL, std::string(fn) + ": NULL bytes");
+  Kv8AttnArgs a{};
+  return kv8_attn_args(fn, cache, batch, q_heads, window, sinks, true, &a, bytes);
+}
+
+qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, const void* Q, int dtype,
+                               int q_heads, int64_t q_stride, float scale, int window, int sinks, void* Y,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_attention";
+  clear_error();
+  Kv8AttnArgs a{};
+  size_t total = 0;
+  QLIN_TRY(kv8_attn_args(fn, cache, batch, q_heads, window, sinks, false, &a, &total));
+  QLIN_TRY(kv8_check_dtype(fn, dtype));
+  if (!Q || !Y) return fail(QLIN_EINVAL, std::string(fn) + ": NULL Q or Y");
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QLIN_EINVAL, std::string(fn) + ": scale must be finite and positive");
+  QLIN_TRY(need_aligned(fn, "Q", Q));
+  QLIN_TRY(need_aligned(fn, "Y", Y));
+  QLIN_TRY(kv8_check_rows(fn, "q_stride", a.c.tokens, q_heads, a.c.dim, q_stride));
+  if (kv8_overlap(Q, kv8_span(a.c.tokens, q_heads, a.c.dim, q_stride), Y,
+                  kv8_span(a.c.tokens, q_heads, a.c.dim, static_cast<int64_t>(q_heads) * a.c.dim)))
+    return fail(QLIN_EINVAL, std::string(fn) + ": Y overlaps Q");
+  QLIN_TRY(need_workspace(fn, workspace, workspace_bytes, total));
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.q_stride = q_stride;
+  a.scale = scale * 1.44269504088896340736f;   // log2(e)
+  a.Y = static_cast<uint16_t*>(Y);
+  if (total) {
+    const WsView ws{static_cast<char*>(workspace), workspace_bytes};
+    a.counters = ws.counters();
+    a.partials = static_cast<float*>(ws.partials());
+  }
+  kv8_attn_launch(a, dtype, stream);
   return check_launch(fn);
 }
 

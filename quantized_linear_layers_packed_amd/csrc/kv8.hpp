@@ -1,0 +1,80 @@
+// The 8-bit paged key/value cache as the kernels see it, and the launchers of
+// its operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/qlin.h"
+#include "workspace.hpp"
+
+namespace qlin {
+
+// Cache and batch with the sizes that the host has checked.
+struct Kv8View {
+  int8_t* k;
+  int8_t* v;
+  float* scales;
+  const int32_t* offsets;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int pages, heads, dim, log_page;
+  int seqs, tokens, table_stride, max_new, max_kv;
+};
+
+// One sequence of the batch: its first token row, its new tokens, the position
+// of the first of them (negative if there are more of them than the sequence
+// is long) and its length.  Everything clamped, so that whatever the device
+// arrays hold, rows stay in 0 .. tokens and positions below the table's end.
+struct Kv8Seq {
+  int row, count, start, len;
+};
+
+__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8View& c, int b) {
+  Kv8Seq s;
+  s.row = min(max(c.offsets[b], 0), c.tokens);
+  s.count = min(max(c.offsets[b + 1], s.row), c.tokens) - s.row;
+  const long long most = static_cast<long long>(c.table_stride) << c.log_page;
+  s.len = static_cast<int>(min(static_cast<long long>(max(c.kv_lens[b], 0)), min(most, 0x7FFF0000LL)));
+  s.start = s.len - s.count;
+  return s;
+}
+
+struct Kv8AppendArgs {
+  Kv8View c;
+  const uint16_t* Q;
+  const uint16_t* K;
+  const uint16_t* V;
+  long long q_stride, k_stride, v_stride;
+  int q_heads;
+  const float* cos;
+  const float* sin;
+  int max_pos, rot, pairs;
+  uint16_t* Q_out;
+};
+
+struct Kv8AttnArgs {
+  Kv8View c;
+  const uint16_t* Q;
+  long long q_stride;
+  int q_heads, group;   // group: query heads that share a key/value head
+  float scale;          // times log2(e)
+  int window, sinks;    // window 0: none (sinks then 0)
+  uint16_t* Y;
+  // the split of long sequences (see kv8_attn.hip)
+  int row_tiles, splits, chunk;
+  int* counters;
+  float* partials;
+};
+
+void kv8_append_launch(const Kv8AppendArgs& a, int dtype, hipStream_t stream);
+void kv8_gather_launch(const Kv8View& c, uint16_t* K, uint16_t* V, int dtype, hipStream_t stream);
+
+// Fills in the split; returns the workspace bytes beyond the counters (0: the
+// call needs no workspace).
+size_t kv8_attn_plan(Kv8AttnArgs* a);
+void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream);
+
+}  // namespace qlin

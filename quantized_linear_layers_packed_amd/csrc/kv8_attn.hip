@@ -1,0 +1,446 @@
+// Attention over the 8-bit paged key/value cache, gfx950: the kernel for few query
+// rows per key/value head (single tokens, draft verification, short prompts).
+//
+//   O[q] = sum_j p_qj v_j / sum_j p_qj,   p_qj = exp2(c_q s_j (q . k_j) - m_q)
+// with the codes k_j, v_j, the page scales s_j (keys) and t_j (values) and
+// c_q = scale log2(e).  One pass with a running reference m_q.
+//
+// A row is one (token, query head) pair; the rows of the query heads that share
+// a key/value head and of all the call's tokens of a sequence are numbered token
+// by token, so one read of the cache serves 16 NT of them.  Each wave walks
+// tiles of 64 positions on its own, with nothing shared and no barrier:
+//   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = K codes, B = Q (in registers)
+//   O^T += V^T P  A = V^T codes, B = P
+// The transposed products leave, in lane (q, g) (q = lane % 16, g = lane / 16),
+// the weights of one row and 16 consecutive tokens 16 g .. 16 g + 15: exactly
+// the B operand of the second product when its contraction index is permuted the
+// same way, so P never leaves the registers, and as pages hold whole runs of 16
+// tokens a lane needs one page scale whatever the page size.  K rows are read in
+// the order that makes this so; V^T is stored with tokens contiguous, so both
+// operands come from memory in 16-byte pieces, without LDS, one tile ahead of
+// their use.
+//
+// Codes become exact fp16 integers: byte + 128 into the low mantissa of 1024
+// (one v_perm for two codes), minus 1152.  The key scale multiplies the
+// fp32 scores; the value scale goes into the weights relative to the largest
+// value scale that the row has seen, r = t_j / t_max (folded into the exponent),
+// so P' = p r is at most 2^kSlack and rounds to fp16 with 11 bits; the sum of
+// weights takes P' / r in fp32.  Products p r below 2^-24 vanish in fp16: next to
+// the row's reference weight and largest values they are below its rounding.
+//
+// The reference m_q only has to be near the maximum: it moves (and the sums are
+// rescaled) when a score exceeds it by more than kSlack, which spares the
+// cross-lane maximum and the rescaling in most tiles.
+//
+// Bound by memory: 2 D bytes a token against 4 D 16 NT matrix flops.
+
+#include <algorithm>
+#include <cmath>
+
+#include "common.hpp"
+#include "device.hpp"
+#include "kv8.hpp"
+#include "splitk.hpp"
+
+namespace qlin {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kTile = 64;                 // positions per wave step
+constexpr float kSlack = 8.0f;            // scores may exceed the reference by 2^8
+constexpr float kNone = -1.0e30f;         // reference of a row that has seen nothing
+constexpr float kLeastRatio = 9.094947e-13f;   // 2^-40: value scales further below t_max count as that
+
+// 8 codes (two words) as 8 fp16 integers, in order.
+__device__ __forceinline__ h8_t codes_f16(uint32_t w0, uint32_t w1) {
+  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
+  const uint32_t p[4] = {__builtin_amdgcn_perm(0x64646464u, x0, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, x0, 0x04030402u),
+                         __builtin_amdgcn_perm(0x64646464u, x1, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, x1, 0x04030402u)};
+  const h2_t off = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
+  h8_t r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const h2_t v = bitcast<h2_t>(p[j]) - off;
+    r[2 * j] = v[0];
+    r[2 * j + 1] = v[1];
+  }
+  return r;
+}
+
+// Maximum and sum over the four lanes q, q + 16, q + 32, q + 48.
+__device__ __forceinline__ float max_over_g(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float sum_over_g(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// The tiles of 64 positions that the rows at positions p0 .. p1 see: those of the
+// first tokens and those from the start of the window of p0.
+struct Tiles {
+  int sinks, first, count;
+  __device__ __forceinline__ Tiles(int p0, int p1, int window, int sink_tokens) {
+    if (p1 < 0) {
+      sinks = first = count = 0;
+      return;
+    }
+    first = window > 0 ? max(0, max(p0, 0) - window + 1) / kTile : 0;
+    sinks = min(sink_tokens > 0 ? (sink_tokens - 1) / kTile + 1 : 0, first);
+    count = sinks + p1 / kTile - first + 1;
+  }
+  __device__ __forceinline__ int operator[](int x) const { return x < sinks ? x : first + x - sinks; }
+};
+
+// 16 NT query rows as B operands: lane (q, g), slice (u, e) holds dimensions
+// 64 u + 16 g + 8 e .. + 7 of row q.  bf16 rows are scaled by a power of two into
+// fp16's range; *mul is what undoes it.
+template <int D, bool BF16>
+__device__ __forceinline__ void load_rows(const uint16_t* row, int g, h8_t (&q)[D / 64][2], float* mul) {
+  uint4 w[D / 64][2];
+#pragma unroll
+  for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) w[u][e] = *reinterpret_cast<const uint4*>(row + 64 * u + 16 * g + 8 * e);
+  if constexpr (!BF16) {
+    *mul = 1.0f;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) q[u][e] = bitcast<h8_t>(w[u][e]);
+  } else {
+    uint32_t most = 0;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = max(most, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+      }
+    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 16, 64)));
+    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 32, 64)));
+    // the row maximum into [2^14, 2^15); rows of zeros, subnormals or with a
+    // value that is not finite stay as they are
+    const int E = static_cast<int>(most >> 7), e14 = E == 0 || E == 255 ? 0 : E - 127 - 14;
+    *mul = ldexpf(1.0f, e14);
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          q[u][e][j] = static_cast<_Float16>(ldexpf(bf16_bits_to_f32(static_cast<uint16_t>(x[j >> 1] >> (16 * (j & 1)))), -e14));
+      }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store2(uint16_t* y, float a, float b) {
+  uint32_t w;
+  if constexpr (BF16) w = bitcast<uint16_t>(static_cast<__bf16>(a)) | (static_cast<uint32_t>(bitcast<uint16_t>(static_cast<__bf16>(b))) << 16);
+  else w = bitcast<uint16_t>(static_cast<_Float16>(a)) | (static_cast<uint32_t>(bitcast<uint16_t>(static_cast<_Float16>(b))) << 16);
+  *reinterpret_cast<uint32_t*>(y) = w;
+}
+
+// Partial result of a split: [16 NT][D] sums, then [16 NT] (reference, sum of weights).
+template <int D, int NT>
+constexpr size_t kPartial = 16 * NT * (D + 2);
+
+// Grid: splits x (sequence, row tile) x key/value heads, heads fastest.
+template <int D, int NT, bool BF16>
+__global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_rows_kernel(const Kv8AttnArgs a) {
+  constexpr int KU = D / 64, DT = D / 16;
+  __shared__ __align__(16) float sums[kWaves][16][D + 4];
+  __shared__ float refs[kWaves][16 * NT], weights[kWaves][16 * NT];
+  __shared__ int flag;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, ql = lane & 15;
+  const int head = blockIdx.x % a.c.heads, unit = blockIdx.x / a.c.heads;
+  const int b = unit / a.row_tiles, split = blockIdx.y;
+  const Kv8Seq seq = kv8_seq(a.c, b);
+  const int P = 1 << a.c.log_page, G = a.group;
+  const long long rows = static_cast<long long>(seq.count) * G;
+  // row tiles past the grid are taken up in turn
+  for (long long r0 = static_cast<long long>(unit % a.row_tiles) * (16 * NT); r0 < rows; r0 += static_cast<long long>(a.row_tiles) * (16 * NT)) {
+    const int nrows = static_cast<int>(min(rows - r0, static_cast<long long>(16 * NT)));
+    const int p0 = seq.start + static_cast<int>(r0 / G), p1 = seq.start + static_cast<int>((r0 + nrows - 1) / G);
+    const Tiles tiles(p0, p1, a.window, a.sinks);
+    // row tiles beyond those planned for are not split: their partial results
+    // would share workspace with the first ones'
+    const bool planned = r0 < static_cast<long long>(a.row_tiles) * (16 * NT);
+    const int per = planned ? max(a.chunk, (tiles.count + a.splits - 1) / a.splits) : max(tiles.count, 1);
+    const int used = max((tiles.count + per - 1) / per, 1);
+    if (split >= used) continue;
+    const int x0 = split * per + wv, x1 = min(split * per + per, tiles.count);
+
+    h8_t qf[NT][KU][2];
+    float cq[NT], m[NT], l[NT], tmax[NT];    // tmax: the largest value scale the row has seen, 0: none yet
+    int pos[NT], low[NT];                    // visible: j <= pos and (j >= low or j < sinks)
+    f32x4_t o[NT][DT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const long long r = r0 + min(16 * n + ql, nrows - 1);
+      const int t = static_cast<int>(r / G), h = head * G + static_cast<int>(r - static_cast<long long>(t) * G);
+      load_rows<D, BF16>(a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(h) * D, g, qf[n], &cq[n]);
+      cq[n] *= a.scale;
+      pos[n] = seq.start + t;
+      low[n] = a.window > 0 ? max(pos[n], 0) - a.window + 1 : 0;
+      m[n] = kNone;
+      l[n] = tmax[n] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[n][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const int low_most = a.window > 0 ? max(p1, 0) - a.window + 1 : 0;
+
+    // Loads of a tile: the pages of this lane's K rows (tokens 16 ((lane / 4) % 4) + ..)
+    // and V rows (tokens 16 g ..).
+    const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
+    const int last_entry = (seq.len - 1) >> a.c.log_page;       // entries past it are not read
+    const int gk = (ql >> 2);
+    const int xl = x0 + (max(x1 - x0, 1) - 1) / kWaves * kWaves;   // this wave's last tile: loads past it repeat it
+    struct Pages { int k, v; };
+    auto load_pages = [&](int x) {
+      const int base = tiles[min(x, xl)] * kTile;
+      return Pages{table[min((base + 16 * gk) >> a.c.log_page, last_entry)], table[min((base + 16 * g) >> a.c.log_page, last_entry)]};
+    };
+    auto valid = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages); };
+    uint4 kw[4][KU], vw[DT];
+    float2 sc;
+    bool held;
+    auto load_k = [&](int x, const Pages& p) {
+      const int base = tiles[min(x, xl)] * kTile;
+      const size_t pk = valid(p.k) ? p.k : 0, pv = valid(p.v) ? p.v : 0;
+      held = valid(p.v);
+      sc = reinterpret_cast<const float2*>(a.c.scales)[pv * a.c.heads + head];   // not looked at unless held
+      const int8_t* src = a.c.k + (((pk * a.c.heads + head) << a.c.log_page) + ((base + 16 * gk) & (P - 1)) + (ql & 3)) * D + 16 * g;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int u = 0; u < KU; ++u) kw[t][u] = *reinterpret_cast<const uint4*>(src + 4 * t * D + 64 * u);
+    };
+    auto load_v = [&](int x, const Pages& p) {
+      const int base = tiles[min(x, xl)] * kTile;
+      const size_t pv = valid(p.v) ? p.v : 0;
+      const int8_t* src = a.c.v + (((pv * a.c.heads + head) * D + ql) << a.c.log_page) + ((base + 16 * g) & (P - 1));
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vw[d] = *reinterpret_cast<const uint4*>(src + (static_cast<size_t>(16 * d) << a.c.log_page));
+    };
+
+    if (x0 < x1) {
+      Pages now = load_pages(x0), next = load_pages(x0 + kWaves);
+      load_k(x0, now);
+      load_v(x0, now);
+      for (int x = x0; x < x1; x += kWaves) {
+        const int base = tiles[x] * kTile, j0 = base + 16 * g;
+        const bool here = held;
+        const float2 s = sc;
+        f32x4_t st[NT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) st[n][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int u = 0; u < KU; ++u) {
+            const h8_t k0 = codes_f16(kw[t][u].x, kw[t][u].y), k1 = codes_f16(kw[t][u].z, kw[t][u].w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              st[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][u][0], st[n][t], 0, 0, 0);
+              st[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][u][1], st[n][t], 0, 0, 0);
+            }
+          }
+        }
+        const Pages coming = next;
+        next = load_pages(x + 2 * kWaves);
+        load_k(x + kWaves, coming);
+
+        // every position of the tile visible to every row, and every page there
+        const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && !__any(!here);
+        h8_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          // the span's value scale, as far as the row sees any of it; a larger one
+          // than so far: rescale the sums to it
+          const float ty = here && j0 <= pos[n] && (j0 + 15 >= low[n] || j0 < a.sinks) ? s.y : 0.0f;
+          if (__any(ty > tmax[n])) {
+            const float was = tmax[n];
+            tmax[n] = fmaxf(was, max_over_g(ty));
+            const float f = was > 0.0f ? was / tmax[n] : 1.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[n][d] *= f;
+          }
+          const float ratio0 = ty / (tmax[n] > 0.0f ? tmax[n] : 1.0f);
+          const float ratio = ratio0 < kLeastRatio ? kLeastRatio : ratio0;      // NaN stays
+          const float lr = __log2f(ratio), unratio = 1.0f / ratio;
+          const float c = s.x * cq[n];
+          float top = kNone;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 4 * t + i;
+              float v = st[n][t][i] * c;
+              if (!full && !(here && j <= pos[n] && (j >= low[n] || j < a.sinks))) v = -INFINITY;
+              st[n][t][i] = v;
+              top = fmaxf(top, v);
+            }
+          if (__any(top > m[n] + kSlack)) {
+            const float was = m[n];
+            const float high = max_over_g(top);
+            m[n] = high > was + kSlack ? high : was;           // by the row's own scores alone
+            const float f = exp2f(was - m[n]);
+            l[n] *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[n][d] *= f;
+          }
+          const float shift = lr - m[n];
+          float part = 0.0f;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float p = __builtin_amdgcn_exp2f(st[n][t][i] + shift);
+              if (!full && st[n][t][i] == -INFINITY) p = 0.0f;
+              part += p;
+              pf[n][t >> 1][4 * (t & 1) + i] = static_cast<_Float16>(p);
+            }
+          l[n] = fmaf(part, unratio, l[n]);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const h8_t v0 = codes_f16(vw[d].x, vw[d].y), v1 = codes_f16(vw[d].z, vw[d].w);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[n][0], o[n][d], 0, 0, 0);
+            o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], o[n][d], 0, 0, 0);
+          }
+        }
+        load_v(x + kWaves, coming);
+      }
+    }
+
+    // Join the waves: references and sums of weights first, then the sums, 16
+    // rows at a time through LDS.
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float all = sum_over_g(l[n]);
+      if (g == 0) {
+        refs[wv][16 * n + ql] = m[n];
+        weights[wv][16 * n + ql] = all;
+      }
+    }
+    __syncthreads();
+    const int tile_unit = blockIdx.x;
+    float* part = a.partials + (static_cast<size_t>(tile_unit) * a.splits + split) * kPartial<D, NT>;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float top = refs[0][16 * n + ql];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, refs[w][16 * n + ql]);
+      const float f = exp2f(m[n] - top) * tmax[n];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(&sums[wv][ql][16 * d + 4 * g]) = o[n][d] * f;
+      __syncthreads();
+      for (int i = tid; i < 16 * D / 2; i += 64 * kWaves) {
+        const int rr = i / (D / 2), d = 2 * (i - rr * (D / 2)), r = 16 * n + rr;
+        if (r >= nrows) break;
+        float ref = refs[0][r];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, refs[w][r]);
+        float total = 0.0f, y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          total = fmaf(weights[w][r], exp2f(refs[w][r] - ref), total);
+          y0 += sums[w][rr][d];
+          y1 += sums[w][rr][d + 1];
+        }
+        if (used == 1) {
+          const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+          const long long row = r0 + r;
+          const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
+          store2<BF16>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d, y0 * inv, y1 * inv);
+        } else {
+          sk_store(part + r * D + d, y0);
+          sk_store(part + r * D + d + 1, y1);
+          if (d == 0) {
+            sk_store(part + 16 * NT * D + 2 * r, ref);
+            sk_store(part + 16 * NT * D + 2 * r + 1, total);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (used == 1) continue;
+
+    // The split that arrives last joins them all, in their order.
+    if (!sk_arrive_last(a.counters + tile_unit, used - 1, &flag)) continue;
+    const float* first = a.partials + static_cast<size_t>(tile_unit) * a.splits * kPartial<D, NT>;
+    for (int i = tid; i < nrows * (D / 2); i += 64 * kWaves) {
+      const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
+      float ref = kNone;
+      for (int k = 0; k < used; ++k) ref = fmaxf(ref, sk_load(first + k * kPartial<D, NT> + 16 * NT * D + 2 * r));
+      float total = 0.0f, y0 = 0.0f, y1 = 0.0f;
+      for (int k = 0; k < used; ++k) {
+        const float* q = first + k * kPartial<D, NT>;
+        const float f = exp2f(sk_load(q + 16 * NT * D + 2 * r) - ref);
+        total = fmaf(sk_load(q + 16 * NT * D + 2 * r + 1), f, total);
+        y0 = fmaf(sk_load(q + r * D + d), f, y0);
+        y1 = fmaf(sk_load(q + r * D + d + 1), f, y1);
+      }
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      const long long row = r0 + r;
+      const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
+      store2<BF16>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d, y0 * inv, y1 * inv);
+    }
+    if (tid == 0) sk_reset(a.counters + tile_unit);
+    __syncthreads();
+  }
+}
+
+template <int D, int NT>
+void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits);
+  if (dtype == QLIN_BF16) hipLaunchKernelGGL((kv8_rows_kernel<D, NT, true>), grid, dim3(64 * kWaves), 0, stream, a);
+  else hipLaunchKernelGGL((kv8_rows_kernel<D, NT, false>), grid, dim3(64 * kWaves), 0, stream, a);
+}
+
+// 16-row column tiles per wave: up to 16 rows 1, otherwise 2 (heads of 256
+// dimensions have registers for one).
+int rows_nt(const Kv8AttnArgs& a) {
+  return static_cast<long long>(a.c.max_new) * a.group <= 16 || a.c.dim > 128 ? 1 : 2;
+}
+
+}  // namespace
+
+size_t kv8_attn_plan(Kv8AttnArgs* a) {
+  const int nt = rows_nt(*a), cus = device_cus();
+  const long long rows = static_cast<long long>(a->c.max_new) * a->group, tile_rows = 16 * nt;
+  const long long most = std::max<long long>(1, (1LL << 23) / (static_cast<long long>(a->c.seqs) * a->c.heads));
+  a->row_tiles = static_cast<int>(std::min((rows + tile_rows - 1) / tile_rows, most));
+  long long tiles = (static_cast<long long>(a->c.max_kv) + kTile - 1) / kTile;
+  if (a->window > 0)
+    tiles = std::min(tiles, (a->window + tile_rows / a->group) / kTile + 2 + (static_cast<long long>(a->sinks) + kTile - 1) / kTile);
+  const long long units = static_cast<long long>(a->c.seqs) * a->row_tiles * a->c.heads;
+  a->splits = 1;
+  a->chunk = static_cast<int>(tiles);
+  if (units > kCounterSlots) return 0;
+  const long long chunk = std::max<long long>(kWaves, (units * tiles + 4 * cus - 1) / (4 * cus));
+  const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, 128);
+  a->splits = static_cast<int>(splits);
+  a->chunk = static_cast<int>((tiles + splits - 1) / splits);
+  return splits == 1 ? 0 : static_cast<size_t>(units) * splits * 16 * nt * (a->c.dim + 2) * sizeof(float);
+}
+
+void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
+  const bool one = rows_nt(a) == 1;
+  switch (a.c.dim) {
+    case 64: one ? rows_launch<64, 1>(a, dtype, stream) : rows_launch<64, 2>(a, dtype, stream); break;
+    case 128: one ? rows_launch<128, 1>(a, dtype, stream) : rows_launch<128, 2>(a, dtype, stream); break;
+    default: rows_launch<256, 1>(a, dtype, stream); break;
+  }
+}
+
+}  // namespace qlin

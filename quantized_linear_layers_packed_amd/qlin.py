@@ -37,6 +37,7 @@ _lib = C.CDLL(LIB_PATH)
 
 QLIN_OK, QLIN_EINVAL, QLIN_EALIGN, QLIN_EUNSUPPORTED, QLIN_EHIP = range(5)
 QLIN_F16, QLIN_BF16, QLIN_F32 = 1, 2, 3
+QLIN_ROPE_HALF, QLIN_ROPE_PAIRS = 0, 1
 
 EXPORTS = (
     "qlin_version", "qlin_status_str", "qlin_last_error",
@@ -48,9 +49,10 @@ EXPORTS = (
     "qlin_w4_pack_gptq_actorder", "qlin_w4_forward_perm",
     "qlin_w4_workspace_bytes", "sq_int8_gemm_workspace_bytes", "qlin_w4_forward_scratch",
     "qlin_mfma_peak", "spqr_workspace_bytes", "qlin_f16_gemm", "qlin_f16_gemm_workspace_bytes",
+    "qlin_kv8_sizes", "qlin_kv8_append", "qlin_kv8_gather", "qlin_kv8_attention", "qlin_kv8_attention_workspace_bytes",
 )
 
-_vp, _i, _i64, _sz, _d = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_double
+_vp, _i, _i64, _sz, _d, _f = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_double, C.c_float
 _sigs = {
     "qlin_version": ([], _i),
     "qlin_status_str": ([_i], C.c_char_p),
@@ -82,6 +84,11 @@ _sigs = {
     "spqr_pack_hessian": ([_vp, _i, _i, _d, _vp, _d, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _i),
     "qlin_w4_pack_gptq_actorder": ([_vp, _i, _i, _i, _vp, _d, _i, _vp, _vp, _vp, _vp], _i),
     "qlin_w4_forward_perm": ([_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _sz, _vp], _i),
+    "qlin_kv8_sizes": ([_i, _i, _i, _i, _vp, _vp, _vp], _i),
+    "qlin_kv8_append": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i64, _i64, _i64, _vp, _vp, _i, _i, _i, _vp, _vp], _i),
+    "qlin_kv8_gather": ([_vp, _vp, _vp, _vp, _i, _vp], _i),
+    "qlin_kv8_attention": ([_vp, _vp, _vp, _i, _i, _i64, _f, _i, _i, _vp, _vp, _sz, _vp], _i),
+    "qlin_kv8_attention_workspace_bytes": ([_vp, _vp, _i, _i, _i, _vp], _i),
 }
 for _name, (_args, _res) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -366,6 +373,123 @@ def qlin_f16_gemm_workspace_bytes(M, N, K, y_dtype=QLIN_F16):
 def qlin_f16_gemm(X, W, M, N, K, Y, y_dtype=QLIN_F16, workspace=None, workspace_bytes=None, stream=None):
     _check(_lib.qlin_f16_gemm(_ptr(X), _ptr(W), M, N, K, _ptr(Y), y_dtype, _ptr(workspace),
                               _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit paged key/value cache
+
+class _KvCache(C.Structure):
+    _fields_ = [("k_codes", _vp), ("v_codes", _vp), ("scales", _vp),
+                ("num_pages", _i), ("kv_heads", _i), ("head_dim", _i), ("page_size", _i)]
+
+
+class _KvBatch(C.Structure):
+    _fields_ = [("offsets", _vp), ("kv_lens", _vp), ("block_table", _vp),
+                ("seqs", _i), ("tokens", _i), ("table_stride", _i), ("max_new", _i), ("max_kv", _i)]
+
+
+class Kv8Cache:
+    """A qlin_kv8_cache over three tensors: k_codes int8 [pages][kv_heads][page_size][head_dim], v_codes int8
+    [pages][kv_heads][head_dim][page_size], scales fp32 [pages][kv_heads][2].  Keeps them alive; make it once."""
+
+    def __init__(self, k_codes, v_codes, scales):
+        pages, heads, page, dim = k_codes.shape
+        if tuple(v_codes.shape) != (pages, heads, dim, page) or tuple(scales.shape) != (pages, heads, 2):
+            raise ValueError(f"v_codes {tuple(v_codes.shape)} and scales {tuple(scales.shape)} do not fit "
+                             f"k_codes {tuple(k_codes.shape)}")
+        for name, t, size in (("k_codes", k_codes, 1), ("v_codes", v_codes, 1), ("scales", scales, 4)):
+            if t.element_size() != size:
+                raise ValueError(f"{name}: {size}-byte values expected")
+        self.tensors = (k_codes, v_codes, scales)
+        self._c = _KvCache(_ptr(k_codes), _ptr(v_codes), _ptr(scales), pages, heads, dim, page)
+        self.ref = C.addressof(self._c)
+        self.kv_heads, self.head_dim = heads, dim
+
+
+class Kv8Batch:
+    """A qlin_kv8_batch: int32 tensors offsets [seqs + 1], kv_lens [seqs], block_table [seqs][table_stride], and the
+    host's counts.  Keeps the tensors alive; their contents may change between calls."""
+
+    def __init__(self, offsets, kv_lens, block_table, tokens, max_new, max_kv):
+        seqs, stride = block_table.shape
+        if tuple(offsets.shape) != (seqs + 1,) or tuple(kv_lens.shape) != (seqs,):
+            raise ValueError(f"offsets {tuple(offsets.shape)} and kv_lens {tuple(kv_lens.shape)} do not fit "
+                             f"block_table {tuple(block_table.shape)}")
+        for name, t in (("offsets", offsets), ("kv_lens", kv_lens), ("block_table", block_table)):
+            if t.element_size() != 4:
+                raise ValueError(f"{name}: int32 expected")
+        self.tensors = (offsets, kv_lens, block_table)
+        self._c = _KvBatch(_ptr(offsets), _ptr(kv_lens), _ptr(block_table), seqs, tokens, stride, max_new, max_kv)
+        self.ref = C.addressof(self._c)
+        self.tokens = tokens
+
+
+def _rows(x, tokens, heads, dim):
+    """(pointer, token stride in elements) of x [tokens][heads][dim], 16-bit, whose tokens may lie apart."""
+    if x is None:
+        return None, 0
+    shape, stride = tuple(x.shape), x.stride()
+    if (shape != (tokens, heads, dim) or x.element_size() != 2 or stride[2] != 1
+            or (heads > 1 and stride[1] != dim)):
+        raise ValueError(f"16-bit [{tokens}][{heads}][{dim}] with contiguous heads expected, got shape {shape}, "
+                         f"strides {tuple(stride)}, {x.element_size()}-byte values")
+    return x.data_ptr(), stride[0] if tokens > 1 else heads * dim
+
+
+def _out(x, tokens, heads, dim):
+    """Pointer of a contiguous 16-bit tensor of tokens * heads * dim values."""
+    if x is not None and (x.numel() != tokens * heads * dim or x.element_size() != 2):
+        raise ValueError(f"{tokens} * {heads} * {dim} 16-bit values expected, got shape {tuple(x.shape)}, "
+                         f"{x.element_size()}-byte values")
+    return _ptr(x)
+
+
+def _table(x, rot_dim):
+    if x is not None and (len(x.shape) != 2 or x.shape[1] != rot_dim // 2 or x.element_size() != 4):
+        raise ValueError(f"fp32 [max_pos][{rot_dim // 2}] expected, got shape {tuple(x.shape)}, "
+                         f"{x.element_size()}-byte values")
+    return _ptr(x)
+
+
+def qlin_kv8_sizes(num_pages, kv_heads, head_dim, page_size):
+    k, v, s = C.c_size_t(), C.c_size_t(), C.c_size_t()
+    _check(_lib.qlin_kv8_sizes(num_pages, kv_heads, head_dim, page_size, C.byref(k), C.byref(v), C.byref(s)))
+    return k.value, v.value, s.value
+
+
+def qlin_kv8_append(cache, batch, Q, K, V, dtype, q_heads, cos, sin, rot_dim, rope_style, Q_out, stream=None):
+    """Q, K, V: tensors [tokens][heads][head_dim], slices of a fused projection's output among them (Q and Q_out may
+    be None); cos, sin: fp32 [max_pos][rot_dim / 2] (None without rotation)."""
+    T, H, D = batch.tokens, cache.kv_heads, cache.head_dim
+    q, q_stride = _rows(Q, T, q_heads, D)
+    k, k_stride = _rows(K, T, H, D)
+    v, v_stride = _rows(V, T, H, D)
+    max_pos = 0 if cos is None or sin is None else min(cos.shape[0], sin.shape[0])
+    _check(_lib.qlin_kv8_append(cache.ref, batch.ref, q, k, v, dtype, q_heads, q_stride, k_stride, v_stride,
+                                _table(cos, rot_dim), _table(sin, rot_dim), max_pos, rot_dim, rope_style,
+                                _out(Q_out, T, q_heads, D), _stream(stream)))
+
+
+def qlin_kv8_gather(cache, batch, K_out, V_out, dtype, stream=None):
+    T, H, D = batch.tokens, cache.kv_heads, cache.head_dim
+    _check(_lib.qlin_kv8_gather(cache.ref, batch.ref, _out(K_out, T, H, D), _out(V_out, T, H, D), dtype,
+                                _stream(stream)))
+
+
+def qlin_kv8_attention_workspace_bytes(cache, batch, q_heads, window=0, sinks=0):
+    b = C.c_size_t()
+    _check(_lib.qlin_kv8_attention_workspace_bytes(cache.ref, batch.ref, q_heads, window, sinks, C.byref(b)))
+    return b.value
+
+
+def qlin_kv8_attention(cache, batch, Q, dtype, q_heads, scale, window, sinks, Y, workspace=None, workspace_bytes=None,
+                       stream=None):
+    """Q: a tensor [tokens][q_heads][head_dim], slices of a fused projection's output among them."""
+    T, D = batch.tokens, cache.head_dim
+    q, q_stride = _rows(Q, T, q_heads, D)
+    _check(_lib.qlin_kv8_attention(cache.ref, batch.ref, q, dtype, q_heads, q_stride, scale, window, sinks,
+                                   _out(Y, T, q_heads, D), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                   _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
