@@ -1,9 +1,9 @@
 // Attention over the 8-bit paged key/value cache, gfx950: the kernel for few query
 // rows per key/value head (single tokens, draft verification, short prompts).
 //
-//   O[q] = sum_j p_qj v_j / sum_j p_qj,   p_qj = exp2(c_q s_j (q . k_j) - m_q)
+//   O[q] = sum_j p_qj t_j v_j / sum_j p_qj,   p_qj = exp2(c_q s_j (q . k_j))
 // with the codes k_j, v_j, the page scales s_j (keys) and t_j (values) and
-// c_q = scale log2(e).  One pass with a running reference m_q.
+// c_q = scale log2(e).  One pass with a running reference m_q (below).
 //
 // A row is one (token, query head) pair; the rows of the query heads that share
 // a key/value head and of all the call's tokens of a sequence are numbered token
@@ -20,15 +20,15 @@
 // operands come from memory in 16-byte pieces, without LDS, one tile ahead of
 // their use.
 //
-// Codes become exact fp16 integers: byte + 128 into the low mantissa of 1024
-// (one v_perm for two codes), minus 1152.  The key scale multiplies the
-// fp32 scores; the value scale goes into the weights relative to the largest
-// value scale that the row has seen, r = t_j / t_max (folded into the exponent),
-// so P' = p r is at most 2^kSlack and rounds to fp16 with 11 bits; the sum of
-// weights takes P' / r in fp32.  Products p r below 2^-24 vanish in fp16: next to
-// the row's reference weight and largest values they are below its rounding.
+// Codes become exact fp16 integers (one v_perm for two codes and one packed
+// subtraction).  The key scale multiplies the fp32 scores.  The value scale t_j
+// goes into the weights, in the exponent: p'_qj = p_qj t_j 2^-m_q, with the
+// reference m_q near the row's maximum of score + log2 t_j, so the largest p' are
+// near 1 and round to fp16 with 11 bits, and what falls below 2^-24 is below the
+// rounding of the largest.  O[q] = sum p' (codes of v) / sum p' / t, the sum of
+// weights in fp32.
 //
-// The reference m_q only has to be near the maximum: it moves (and the sums are
+// The reference only has to be near the maximum: it moves (and the sums are
 // rescaled) when a score exceeds it by more than kSlack, which spares the
 // cross-lane maximum and the rescaling in most tiles.
 //
@@ -40,6 +40,7 @@
 #include "common.hpp"
 #include "device.hpp"
 #include "kv8.hpp"
+#include "kv8_device.hpp"
 #include "splitk.hpp"
 
 namespace qlin {
@@ -47,27 +48,6 @@ namespace qlin {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kTile = 64;                 // positions per wave step
-constexpr float kSlack = 8.0f;            // scores may exceed the reference by 2^8
-constexpr float kNone = -1.0e30f;         // reference of a row that has seen nothing
-constexpr float kLeastRatio = 9.094947e-13f;   // 2^-40: value scales further below t_max count as that
-
-// 8 codes (two words) as 8 fp16 integers, in order.
-__device__ __forceinline__ h8_t codes_f16(uint32_t w0, uint32_t w1) {
-  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
-  const uint32_t p[4] = {__builtin_amdgcn_perm(0x64646464u, x0, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, x0, 0x04030402u),
-                         __builtin_amdgcn_perm(0x64646464u, x1, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, x1, 0x04030402u)};
-  const h2_t off = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
-  h8_t r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const h2_t v = bitcast<h2_t>(p[j]) - off;
-    r[2 * j] = v[0];
-    r[2 * j + 1] = v[1];
-  }
-  return r;
-}
-
 // Maximum and sum over the four lanes q, q + 16, q + 32, q + 48.
 __device__ __forceinline__ float max_over_g(float v) {
   v = fmaxf(v, __shfl_xor(v, 16, 64));
@@ -77,22 +57,6 @@ __device__ __forceinline__ float sum_over_g(float v) {
   v += __shfl_xor(v, 16, 64);
   return v + __shfl_xor(v, 32, 64);
 }
-
-// The tiles of 64 positions that the rows at positions p0 .. p1 see: those of the
-// first tokens and those from the start of the window of p0.
-struct Tiles {
-  int sinks, first, count;
-  __device__ __forceinline__ Tiles(int p0, int p1, int window, int sink_tokens) {
-    if (p1 < 0) {
-      sinks = first = count = 0;
-      return;
-    }
-    first = window > 0 ? max(0, max(p0, 0) - window + 1) / kTile : 0;
-    sinks = min(sink_tokens > 0 ? (sink_tokens - 1) / kTile + 1 : 0, first);
-    count = sinks + p1 / kTile - first + 1;
-  }
-  __device__ __forceinline__ int operator[](int x) const { return x < sinks ? x : first + x - sinks; }
-};
 
 // 16 NT query rows as B operands: lane (q, g), slice (u, e) holds dimensions
 // 64 u + 16 g + 8 e .. + 7 of row q.  bf16 rows are scaled by a power of two into
@@ -115,35 +79,16 @@ __device__ __forceinline__ void load_rows(const uint16_t* row, int g, h8_t (&q)[
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) most = max(most, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-      }
+      for (int e = 0; e < 2; ++e) most = max(most, chunk_most(w[u][e]));
     most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 16, 64)));
     most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 32, 64)));
-    // the row maximum into [2^14, 2^15); rows of zeros, subnormals or with a
-    // value that is not finite stay as they are
-    const int E = static_cast<int>(most >> 7), e14 = E == 0 || E == 255 ? 0 : E - 127 - 14;
+    const int e14 = row_exponent(most);
     *mul = ldexpf(1.0f, e14);
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          q[u][e][j] = static_cast<_Float16>(ldexpf(bf16_bits_to_f32(static_cast<uint16_t>(x[j >> 1] >> (16 * (j & 1)))), -e14));
-      }
+      for (int e = 0; e < 2; ++e) q[u][e] = chunk_f16(w[u][e], e14);
   }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store2(uint16_t* y, float a, float b) {
-  uint32_t w;
-  if constexpr (BF16) w = bitcast<uint16_t>(static_cast<__bf16>(a)) | (static_cast<uint32_t>(bitcast<uint16_t>(static_cast<__bf16>(b))) << 16);
-  else w = bitcast<uint16_t>(static_cast<_Float16>(a)) | (static_cast<uint32_t>(bitcast<uint16_t>(static_cast<_Float16>(b))) << 16);
-  *reinterpret_cast<uint32_t*>(y) = w;
 }
 
 // Partial result of a split: [16 NT][D] sums, then [16 NT] (reference, sum of weights).
@@ -167,7 +112,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
   for (long long r0 = static_cast<long long>(unit % a.row_tiles) * (16 * NT); r0 < rows; r0 += static_cast<long long>(a.row_tiles) * (16 * NT)) {
     const int nrows = static_cast<int>(min(rows - r0, static_cast<long long>(16 * NT)));
     const int p0 = seq.start + static_cast<int>(r0 / G), p1 = seq.start + static_cast<int>((r0 + nrows - 1) / G);
-    const Tiles tiles(p0, p1, a.window, a.sinks);
+    const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
     // row tiles beyond those planned for are not split: their partial results
     // would share workspace with the first ones'
     const bool planned = r0 < static_cast<long long>(a.row_tiles) * (16 * NT);
@@ -177,7 +122,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
     const int x0 = split * per + wv, x1 = min(split * per + per, tiles.count);
 
     h8_t qf[NT][KU][2];
-    float cq[NT], m[NT], l[NT], tmax[NT];    // tmax: the largest value scale the row has seen, 0: none yet
+    float cq[NT], m[NT], l[NT];
     int pos[NT], low[NT];                    // visible: j <= pos and (j >= low or j < sinks)
     f32x4_t o[NT][DT];
 #pragma unroll
@@ -189,7 +134,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
       pos[n] = seq.start + t;
       low[n] = a.window > 0 ? max(pos[n], 0) - a.window + 1 : 0;
       m[n] = kNone;
-      l[n] = tmax[n] = 0.0f;
+      l[n] = 0.0f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[n][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -258,55 +203,47 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
 
         // every position of the tile visible to every row, and every page there
         const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && !__any(!here);
+        const float vs = s.y < kLeastScale ? kLeastScale : s.y;                // NaN stays
+        const float lv = __log2f(vs), iv = 1.0f / vs;
         h8_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          // the span's value scale, as far as the row sees any of it; a larger one
-          // than so far: rescale the sums to it
-          const float ty = here && j0 <= pos[n] && (j0 + 15 >= low[n] || j0 < a.sinks) ? s.y : 0.0f;
-          if (__any(ty > tmax[n])) {
-            const float was = tmax[n];
-            tmax[n] = fmaxf(was, max_over_g(ty));
-            const float f = was > 0.0f ? was / tmax[n] : 1.0f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[n][d] *= f;
-          }
-          const float ratio0 = ty / (tmax[n] > 0.0f ? tmax[n] : 1.0f);
-          const float ratio = ratio0 < kLeastRatio ? kLeastRatio : ratio0;      // NaN stays
-          const float lr = __log2f(ratio), unratio = 1.0f / ratio;
           const float c = s.x * cq[n];
+          const uint32_t seen = full ? 0xFFFFu : visible_bits<16>(j0, pos[n], low[n], a.sinks, here);
           float top = kNone;
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = j0 + 4 * t + i;
-              float v = st[n][t][i] * c;
-              if (!full && !(here && j <= pos[n] && (j >= low[n] || j < a.sinks))) v = -INFINITY;
-              st[n][t][i] = v;
-              top = fmaxf(top, v);
-            }
+            for (int i = 0; i < 4; ++i) st[n][t][i] = fmaf(st[n][t][i], c, lv);
+          if (!full) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st[n][t][i] = (seen >> (4 * t + i)) & 1u ? st[n][t][i] : -INFINITY;
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, st[n][t][i]);
           if (__any(top > m[n] + kSlack)) {
             const float was = m[n];
             const float high = max_over_g(top);
             m[n] = high > was + kSlack ? high : was;           // by the row's own scores alone
-            const float f = exp2f(was - m[n]);
+            const float f = __builtin_amdgcn_exp2f(was - m[n]);
             l[n] *= f;
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[n][d] *= f;
           }
-          const float shift = lr - m[n];
           float part = 0.0f;
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float p = __builtin_amdgcn_exp2f(st[n][t][i] + shift);
-              if (!full && st[n][t][i] == -INFINITY) p = 0.0f;
+              const float p = __builtin_amdgcn_exp2f(st[n][t][i] - m[n]);   // hidden: exp2(-inf) = 0
               part += p;
               pf[n][t >> 1][4 * (t & 1) + i] = static_cast<_Float16>(p);
             }
-          l[n] = fmaf(part, unratio, l[n]);
+          l[n] = fmaf(part, seen != 0 ? iv : 0.0f, l[n]);          // a hidden page's scale may be NaN
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -340,7 +277,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
       float top = refs[0][16 * n + ql];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) top = fmaxf(top, refs[w][16 * n + ql]);
-      const float f = exp2f(m[n] - top) * tmax[n];
+      const float f = exp2f(m[n] - top);
 #pragma unroll
       for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(&sums[wv][ql][16 * d + 4 * g]) = o[n][d] * f;
       __syncthreads();
@@ -361,7 +298,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
           const float inv = total == 0.0f ? 0.0f : 1.0f / total;
           const long long row = r0 + r;
           const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
-          store2<BF16>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d, y0 * inv, y1 * inv);
+          *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
         } else {
           sk_store(part + r * D + d, y0);
           sk_store(part + r * D + d + 1, y1);
@@ -393,7 +330,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
       const float inv = total == 0.0f ? 0.0f : 1.0f / total;
       const long long row = r0 + r;
       const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
-      store2<BF16>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d, y0 * inv, y1 * inv);
+      *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
     }
     if (tid == 0) sk_reset(a.counters + tile_unit);
     __syncthreads();
@@ -407,18 +344,19 @@ void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   else hipLaunchKernelGGL((kv8_rows_kernel<D, NT, false>), grid, dim3(64 * kWaves), 0, stream, a);
 }
 
-// 16-row column tiles per wave: up to 16 rows 1, otherwise 2 (heads of 256
-// dimensions have registers for one).
+// 16-row column tiles per wave of the kernel for few rows, 0 for the kernel for
+// many rows.  Heads of 256 dimensions have registers for one.
 int rows_nt(const Kv8AttnArgs& a) {
-  return static_cast<long long>(a.c.max_new) * a.group <= 16 || a.c.dim > 128 ? 1 : 2;
+  const long long rows = static_cast<long long>(a.c.max_new) * a.group;
+  return rows <= 16 ? 1 : rows <= 32 && a.c.dim <= 128 ? 2 : 0;
 }
 
 }  // namespace
 
 size_t kv8_attn_plan(Kv8AttnArgs* a) {
   const int nt = rows_nt(*a), cus = device_cus();
-  const long long rows = static_cast<long long>(a->c.max_new) * a->group, tile_rows = 16 * nt;
-  const long long most = std::max<long long>(1, (1LL << 23) / (static_cast<long long>(a->c.seqs) * a->c.heads));
+  const long long rows = static_cast<long long>(a->c.max_new) * a->group, tile_rows = nt ? 16 * nt : kv8_prompt_rows(a->c.dim);
+  const long long most = std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads));
   a->row_tiles = static_cast<int>(std::min((rows + tile_rows - 1) / tile_rows, most));
   long long tiles = (static_cast<long long>(a->c.max_kv) + kTile - 1) / kTile;
   if (a->window > 0)
@@ -427,18 +365,25 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   a->splits = 1;
   a->chunk = static_cast<int>(tiles);
   if (units > kCounterSlots) return 0;
-  const long long chunk = std::max<long long>(kWaves, (units * tiles + 4 * cus - 1) / (4 * cus));
+  const long long chunk = nt ? std::max<long long>(kWaves, (units * tiles + 4 * cus - 1) / (4 * cus))
+                             : std::max<long long>(8, (units * tiles + 2 * cus - 1) / (2 * cus));
   const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, 128);
   a->splits = static_cast<int>(splits);
   a->chunk = static_cast<int>((tiles + splits - 1) / splits);
-  return splits == 1 ? 0 : static_cast<size_t>(units) * splits * 16 * nt * (a->c.dim + 2) * sizeof(float);
+  if (splits == 1) return 0;
+  const size_t partial = nt ? static_cast<size_t>(tile_rows) * (a->c.dim + 2) * sizeof(float) : kv8_prompt_partial(a->c.dim);
+  return static_cast<size_t>(units) * splits * partial;
 }
 
 void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
-  const bool one = rows_nt(a) == 1;
+  const int nt = rows_nt(a);
+  if (nt == 0) {
+    kv8_prompt_launch(a, dtype, stream);
+    return;
+  }
   switch (a.c.dim) {
-    case 64: one ? rows_launch<64, 1>(a, dtype, stream) : rows_launch<64, 2>(a, dtype, stream); break;
-    case 128: one ? rows_launch<128, 1>(a, dtype, stream) : rows_launch<128, 2>(a, dtype, stream); break;
+    case 64: nt == 1 ? rows_launch<64, 1>(a, dtype, stream) : rows_launch<64, 2>(a, dtype, stream); break;
+    case 128: nt == 1 ? rows_launch<128, 1>(a, dtype, stream) : rows_launch<128, 2>(a, dtype, stream); break;
     default: rows_launch<256, 1>(a, dtype, stream); break;
   }
 }

@@ -1,0 +1,89 @@
+// Device helpers that the 8-bit cache's attention kernels share.
+#pragma once
+
+#include "common.hpp"
+#include "device.hpp"
+#include "kv8.hpp"
+
+namespace qlin {
+
+constexpr int kTile = 64;                      // positions per step of a wave or workgroup
+constexpr float kSlack = 8.0f;                 // scores may exceed the row's reference by 2^8
+constexpr float kNone = -1.0e30f;              // reference of a row that has seen nothing
+constexpr float kLeastScale = 7.8886091e-31f;  // 2^-100: smaller value scales (0 among them) count as that
+
+// 8 codes (two words) as 8 fp16 integers, in order: byte + 128 into the low
+// mantissa of 1024, minus 1152.
+__device__ __forceinline__ h8_t codes_f16(uint32_t w0, uint32_t w1) {
+  const uint32_t x0 = w0 ^ 0x80808080u, x1 = w1 ^ 0x80808080u;
+  const uint32_t p[4] = {__builtin_amdgcn_perm(0x64646464u, x0, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, x0, 0x04030402u),
+                         __builtin_amdgcn_perm(0x64646464u, x1, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, x1, 0x04030402u)};
+  const h2_t off = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
+  h8_t r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const h2_t v = bitcast<h2_t>(p[j]) - off;
+    r[2 * j] = v[0];
+    r[2 * j + 1] = v[1];
+  }
+  return r;
+}
+
+// The tiles of 64 positions that the rows at positions p0 .. p1 see: those of the
+// first tokens and those from the start of the window of p0.
+struct Kv8Tiles {
+  int sinks, first, count;
+  __device__ __forceinline__ Kv8Tiles(int p0, int p1, int window, int sink_tokens) {
+    if (p1 < 0) {
+      sinks = first = count = 0;
+      return;
+    }
+    first = window > 0 ? max(0, max(p0, 0) - window + 1) / kTile : 0;
+    sinks = min(sink_tokens > 0 ? (sink_tokens - 1) / kTile + 1 : 0, first);
+    count = sinks + p1 / kTile - first + 1;
+  }
+  __device__ __forceinline__ int operator[](int x) const { return x < sinks ? x : first + x - sinks; }
+};
+
+// Which of the N consecutive positions from j0 the row at `pos` sees, as bits
+// (low: first position of its window).
+template <int N>
+__device__ __forceinline__ uint32_t visible_bits(int j0, int pos, int low, int sinks, bool held) {
+  const auto below = [&](int end) { return (1u << min(max(end - j0, 0), N)) - 1u; };   // positions before `end`
+  const uint32_t seen = below(pos + 1) & (~below(low) | below(sinks));
+  return held ? seen : 0u;
+}
+
+// Power of two that brings a row of bf16 values with largest magnitude bits
+// `most` into fp16's range: the row maximum into [2^14, 2^15).  Rows of zeros,
+// subnormals or with a value that is not finite stay as they are.
+__device__ __forceinline__ int row_exponent(uint32_t most) {
+  const int E = static_cast<int>(most >> 7);
+  return E == 0 || E == 255 ? 0 : E - 127 - 14;
+}
+__device__ __forceinline__ uint32_t chunk_most(const uint4& w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) most = max(most, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+  return most;
+}
+__device__ __forceinline__ h8_t chunk_f16(const uint4& w, int e) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  h8_t q;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    q[j] = static_cast<_Float16>(ldexpf(bf16_bits_to_f32(static_cast<uint16_t>(x[j >> 1] >> (16 * (j & 1)))), -e));
+  return q;
+}
+
+// Values rounded to the output type, two to a word.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF16)
+    return bitcast<uint16_t>(static_cast<__bf16>(a)) | (static_cast<uint32_t>(bitcast<uint16_t>(static_cast<__bf16>(b))) << 16);
+  else
+    return bitcast<uint16_t>(static_cast<_Float16>(a)) | (static_cast<uint32_t>(bitcast<uint16_t>(static_cast<_Float16>(b))) << 16);
+}
+
+}  // namespace qlin

@@ -1,0 +1,325 @@
+// Attention over the 8-bit paged key/value cache, gfx950: the kernel for many query
+// rows per key/value head (prompts and chunks of prompts).
+//
+// The mathematics and the transposed products are those of the kernel for few
+// rows (kv8_attn.hip), on the 32x32x16 matrix instruction: a workgroup of W waves
+// holds 32 W rows (token by token, the query heads that share a key/value head
+// next to each other), walks the tiles of 64 positions that any of them sees and
+// shares each tile through LDS: every thread converts its part of the next
+// tile's codes to fp16 once, while the waves multiply the present one.
+//   S^T = K Q^T  lane (q, h) (q = lane % 32, h = lane / 32) gets, of each run of 16
+//   O^T += V^T P tokens, the weights of tokens 8 h .. 8 h + 7 for row q: the B
+//                operand of the second product as it stands, because K's rows are
+//                fed in the order that makes it so.
+// A run of 16 tokens lies in one page: its two scales are the same for the whole
+// wave and come as scalars.
+
+#include <algorithm>
+
+#include "common.hpp"
+#include "device.hpp"
+#include "kv8.hpp"
+#include "kv8_device.hpp"
+#include "splitk.hpp"
+
+namespace qlin {
+
+namespace {
+
+template <int D>
+constexpr int kPromptWaves = D == 128 ? 8 : 4;
+
+// fp16 tiles in LDS, rows padded by 16 bytes so that 16 lanes reading 16 bytes
+// each of consecutive rows hit every bank once.
+template <int D>
+struct Tile16 {
+  _Float16 k[kTile][D + 8];
+  _Float16 v[D][kTile + 8];
+};
+
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * kPromptWaves<D>, D > 128 ? 1 : 2) void kv8_prompt_kernel(const Kv8AttnArgs a) {
+  constexpr int W = kPromptWaves<D>, NT = 64 * W, ROWS = 32 * W, DT = D / 32, KS = D / 16;
+  constexpr int NL = D * kTile / 16 / NT;                  // 16-byte pieces of K (and of V) per thread and tile
+  constexpr int SLOT = W * 64 * (16 * DT + 2);             // floats of a split's partial result
+  extern __shared__ __align__(16) char smem[];
+  Tile16<D>* tile = reinterpret_cast<Tile16<D>*>(smem);    // two of them
+  __shared__ int flag;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, h = lane >> 5, ql = lane & 31;
+  const int head = blockIdx.x % a.c.heads, unit = blockIdx.x / a.c.heads;
+  const int b = unit / a.row_tiles, split = blockIdx.y;
+  const Kv8Seq seq = kv8_seq(a.c, b);
+  const int P = 1 << a.c.log_page, G = a.group;
+  const long long rows = static_cast<long long>(seq.count) * G;
+  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
+  const int last_entry = (seq.len - 1) >> a.c.log_page;    // entries past it are not read
+
+  // Row tiles from the last, which sees the most, to the first; row tiles past
+  // the grid are taken up in turn.
+  for (long long r0 = static_cast<long long>(a.row_tiles - 1 - unit % a.row_tiles) * ROWS; r0 < rows;
+       r0 += static_cast<long long>(a.row_tiles) * ROWS) {
+    const int nrows = static_cast<int>(min(rows - r0, static_cast<long long>(ROWS)));
+    const int p0 = seq.start + static_cast<int>(r0 / G), p1 = seq.start + static_cast<int>((r0 + nrows - 1) / G);
+    const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
+    // row tiles beyond those planned for are not split: their partial results
+    // would share workspace with the first ones'
+    const bool planned = r0 < static_cast<long long>(a.row_tiles) * ROWS;
+    const int per = planned ? max(a.chunk, (tiles.count + a.splits - 1) / a.splits) : max(tiles.count, 1);
+    const int used = max((tiles.count + per - 1) / per, 1);
+    if (split >= used) continue;
+    const int x0 = split * per, x1 = min(x0 + per, tiles.count);
+
+    // this lane's row
+    const long long r = r0 + min(32 * wv + ql, nrows - 1);
+    const int t = static_cast<int>(r / G), hq = head * G + static_cast<int>(r - static_cast<long long>(t) * G);
+    const bool mine = 32 * wv + ql < nrows;
+    const int pos = seq.start + t, low = a.window > 0 ? max(pos, 0) - a.window + 1 : 0;
+    const int low_most = a.window > 0 ? max(p1, 0) - a.window + 1 : 0;
+    h8_t qf[KS];                                            // slice s: dimensions 16 s + 8 h .. + 7
+    float cq = a.scale;
+    {
+      const uint16_t* row = a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(hq) * D + 8 * h;
+      if constexpr (BF16) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) most = max(most, chunk_most(*reinterpret_cast<const uint4*>(row + 16 * s)));
+        most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 32, 64)));
+        const int e = row_exponent(most);
+        cq *= ldexpf(1.0f, e);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = chunk_f16(*reinterpret_cast<const uint4*>(row + 16 * s), e);
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const h8_t*>(row + 16 * s);
+      }
+    }
+    f32x16_t o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+    float m = kNone, l = 0.0f;
+
+    auto valid = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages); };
+    auto page_at = [&](int position) { return table[min(position >> a.c.log_page, last_entry)]; };
+
+    // Codes of a tile on their way to LDS, the page entries of the tile after it,
+    // and the scales of the tile's four runs of 16 tokens (lane % 4).
+    uint4 kw[NL], vw[NL];
+    int kpage[NL], vpage[NL], spage;
+    float run_k, run_lv, run_iv;
+    bool run_held;
+    auto load_pages = [&](int x) {
+      const int base = tiles[min(x, x1 - 1)] * kTile;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        kpage[n] = page_at(base + (tid + n * NT) / (D / 16));
+        vpage[n] = page_at(base + 16 * ((tid + n * NT) % 4));
+      }
+      spage = page_at(base + 16 * (lane & 3));
+    };
+    float2 scale2;
+    auto load_codes = [&](int x) {
+      const int base = tiles[min(x, x1 - 1)] * kTile;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        const int i = tid + n * NT, token = i / (D / 16), c = i % (D / 16);
+        const size_t pk = (static_cast<size_t>(valid(kpage[n]) ? kpage[n] : 0) * a.c.heads + head) << a.c.log_page;
+        kw[n] = *reinterpret_cast<const uint4*>(a.c.k + (pk + ((base + token) & (P - 1))) * D + 16 * c);
+        const size_t pv = (static_cast<size_t>(valid(vpage[n]) ? vpage[n] : 0) * a.c.heads + head) * D + i / 4;
+        vw[n] = *reinterpret_cast<const uint4*>(a.c.v + (pv << a.c.log_page) + ((base + 16 * (i % 4)) & (P - 1)));
+      }
+      run_held = valid(spage);
+      scale2 = reinterpret_cast<const float2*>(a.c.scales)[static_cast<size_t>(run_held ? spage : 0) * a.c.heads + head];
+    };
+    auto put_codes = [&](Tile16<D>& to) {
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        const int i = tid + n * NT, token = i / (D / 16), c = i % (D / 16);
+        *reinterpret_cast<h8_t*>(&to.k[token][16 * c]) = codes_f16(kw[n].x, kw[n].y);
+        *reinterpret_cast<h8_t*>(&to.k[token][16 * c + 8]) = codes_f16(kw[n].z, kw[n].w);
+        *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4)]) = codes_f16(vw[n].x, vw[n].y);
+        *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4) + 8]) = codes_f16(vw[n].z, vw[n].w);
+      }
+      const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;       // NaN stays
+      run_k = scale2.x;
+      run_lv = __log2f(vs);
+      run_iv = 1.0f / vs;
+    };
+
+    if (x0 < x1) {
+      load_pages(x0);
+      load_codes(x0);
+      load_pages(x0 + 1);
+      put_codes(tile[0]);
+    }
+    // K row that this lane feeds to row `lane % 32` of a 32-token product
+    const int krow = 16 * (ql >> 4) + 8 * ((ql >> 2) & 1) + 4 * ((ql >> 3) & 1) + (ql & 3);
+    for (int x = x0; x < x1; ++x) {
+      const Tile16<D>& now = tile[(x - x0) & 1];
+      const int base = tiles[x] * kTile;
+      // the runs' scales as scalars (lane s holds run s)
+      float ks[4], lv[4], iv[4];
+      bool held[4], all_held = true;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        ks[s] = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(run_k), s));
+        lv[s] = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(run_lv), s));
+        iv[s] = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(run_iv), s));
+        held[s] = __builtin_amdgcn_readlane(run_held, s) != 0;
+        all_held = all_held && held[s];
+      }
+      load_codes(x + 1);
+      load_pages(x + 2);
+      __syncthreads();                                      // the tile is complete, and the other one is free
+
+      f32x16_t st[2];
+#pragma unroll
+      for (int T = 0; T < 2; ++T) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st[T][i] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          st[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.k[32 * T + krow][16 * s + 8 * h]), qf[s],
+                                                         st[T], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && all_held;
+      uint32_t seen[4];                                     // bit i of run s: this lane's token i
+      if (!full) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          seen[s] = visible_bits<8>(base + 16 * s + 8 * h, pos, low, a.sinks, held[s]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : -INFINITY;
+        }
+      }
+      // run s: values st[s / 2][8 (s % 2) .. + 7]
+      float c[4], top = kNone;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        c[s] = ks[s] * cq;
+        float mx = st[s >> 1][8 * (s & 1)];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, st[s >> 1][8 * (s & 1) + i]);
+        top = fmaxf(top, fmaf(mx, c[s], lv[s]));
+      }
+      if (__any(top > m + kSlack)) {
+        const float high = fmaxf(top, __shfl_xor(top, 32, 64)), was = m;
+        m = high > was + kSlack ? high : was;               // by the row's own scores alone
+        const float f = __builtin_amdgcn_exp2f(was - m);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float shift = lv[s] - m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = 8 * (s & 1) + i;
+          st[s >> 1][k] = __builtin_amdgcn_exp2f(fmaf(st[s >> 1][k], c[s], shift));
+        }
+      }
+      if (!full) {                                          // scales of hidden pages may be anything, NaN among it
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          iv[s] = seen[s] != 0 ? iv[s] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : 0.0f;
+        }
+      }
+      h8_t pf[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = st[s >> 1][8 * (s & 1) + i];
+          part += p;
+          pf[s][i] = static_cast<_Float16>(p);
+        }
+        l = fmaf(part, iv[s], l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.v[32 * d + ql][16 * s + 8 * h]), pf[s],
+                                                        o[d], 0, 0, 0);
+      put_codes(tile[(x - x0 + 1) & 1]);
+    }
+    l += __shfl_xor(l, 32, 64);
+
+    if (used > 1) {
+      // every value of the partial result at its register's and lane's own place
+      float* slots = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * SLOT + wv * 64 * (16 * DT + 2) + lane;
+      asm volatile("" : "+v"(slots));                       // its 16 DT offsets are not to be held through the loop
+      float* part = slots + static_cast<size_t>(split) * SLOT;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sk_store(part + 64 * (16 * d + i), o[d][i]);
+      sk_store(part + 64 * 16 * DT, m);
+      sk_store(part + 64 * 16 * DT + 64, l);
+      if (!sk_arrive_last(a.counters + blockIdx.x, used - 1, &flag)) continue;
+      m = kNone;
+      for (int k = 0; k < used; ++k) m = fmaxf(m, sk_load(slots + static_cast<size_t>(k) * SLOT + 64 * 16 * DT));
+      l = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+      for (int k = 0; k < used; ++k) {
+        const float* q = slots + static_cast<size_t>(k) * SLOT;
+        const float f = __builtin_amdgcn_exp2f(sk_load(q + 64 * 16 * DT) - m);
+        l = fmaf(sk_load(q + 64 * 16 * DT + 64), f, l);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] = fmaf(sk_load(q + 64 * (16 * d + i)), f, o[d][i]);
+          __builtin_amdgcn_sched_barrier(0);                // at most 16 loads' registers
+        }
+      }
+      if (tid == 0) sk_reset(a.counters + blockIdx.x);
+    }
+    if (mine) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + 4 * h;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<uint2*>(y + 32 * d + 2 * i) =
+              make_uint2(pack2<BF16>(o[d][i] * inv, o[d][i + 1] * inv), pack2<BF16>(o[d][i + 2] * inv, o[d][i + 3] * inv));
+    }
+    __syncthreads();                                        // tiles and flag may be used for the next rows
+  }
+}
+
+template <int D>
+void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * kPromptWaves<D>);
+  const size_t lds = 2 * sizeof(Tile16<D>);
+  const auto fn = dtype == QLIN_BF16 ? kv8_prompt_kernel<D, true> : kv8_prompt_kernel<D, false>;
+  hipLaunchKernelGGL(fn, grid, block, lds, stream, a);
+}
+
+}  // namespace
+
+int kv8_prompt_rows(int dim) { return 32 * (dim == 64 ? kPromptWaves<64> : dim == 128 ? kPromptWaves<128> : kPromptWaves<256>); }
+
+size_t kv8_prompt_partial(int dim) { return static_cast<size_t>(kv8_prompt_rows(dim)) * 2 * (dim / 2 + 2) * sizeof(float); }
+
+void kv8_prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
+  switch (a.c.dim) {
+    case 64: prompt_launch<64>(a, dtype, stream); break;
+    case 128: prompt_launch<128>(a, dtype, stream); break;
+    default: prompt_launch<256>(a, dtype, stream); break;
+  }
+}
+
+}  // namespace qlin
