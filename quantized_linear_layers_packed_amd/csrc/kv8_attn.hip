@@ -48,6 +48,7 @@ namespace qlin {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kMostSplits = 64;           // a lane each when they are joined
 // Maximum and sum over the four lanes q, q + 16, q + 32, q + 48.
 __device__ __forceinline__ float max_over_g(float v) {
   v = fmaxf(v, __shfl_xor(v, 16, 64));
@@ -300,37 +301,48 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
           const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
           *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
         } else {
-          sk_store(part + r * D + d, y0);
-          sk_store(part + r * D + d + 1, y1);
-          if (d == 0) {
-            sk_store(part + 16 * NT * D + 2 * r, ref);
-            sk_store(part + 16 * NT * D + 2 * r + 1, total);
-          }
+          sk_store2(part + r * D + d, y0, y1);
+          if (d == 0) sk_store2(part + 16 * NT * D + 2 * r, ref, total);
         }
       }
       __syncthreads();
     }
     if (used == 1) continue;
 
-    // The split that arrives last joins them all, in their order.
+    // The split that arrives last joins them all, in their order: a wave per row
+    // weighs the splits (one per lane), then every thread sums a pair of values.
     if (!sk_arrive_last(a.counters + tile_unit, used - 1, &flag)) continue;
     const float* first = a.partials + static_cast<size_t>(tile_unit) * a.splits * kPartial<D, NT>;
+    float* weigh = &sums[0][0][0];                            // [row][split], the rows' factors after them
+    float* factor = weigh + 16 * NT * kMostSplits;
+    for (int r = wv; r < nrows; r += kWaves) {
+      const float2 mine = lane < used ? sk_load2(first + lane * kPartial<D, NT> + 16 * NT * D + 2 * r) : make_float2(kNone, 0.0f);
+      const float f = __builtin_amdgcn_exp2f(mine.x - wave_max(mine.x));
+      weigh[r * kMostSplits + lane] = f;
+      const float total = wave_sum(mine.y * f);
+      if (lane == 0) factor[r] = total == 0.0f ? 0.0f : 1.0f / total;
+    }
+    __syncthreads();
     for (int i = tid; i < nrows * (D / 2); i += 64 * kWaves) {
       const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
-      float ref = kNone;
-      for (int k = 0; k < used; ++k) ref = fmaxf(ref, sk_load(first + k * kPartial<D, NT> + 16 * NT * D + 2 * r));
-      float total = 0.0f, y0 = 0.0f, y1 = 0.0f;
-      for (int k = 0; k < used; ++k) {
-        const float* q = first + k * kPartial<D, NT>;
-        const float f = exp2f(sk_load(q + 16 * NT * D + 2 * r) - ref);
-        total = fmaf(sk_load(q + 16 * NT * D + 2 * r + 1), f, total);
-        y0 = fmaf(sk_load(q + r * D + d), f, y0);
-        y1 = fmaf(sk_load(q + r * D + d + 1), f, y1);
+      const float* src = first + r * D + d;
+      const float* f = weigh + r * kMostSplits;
+      float y0 = 0.0f, y1 = 0.0f;
+      constexpr int AHEAD = 16;                               // loads in flight
+      for (int k = 0; k < used; k += AHEAD) {
+        float2 v[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) v[j] = sk_load2(src + min(k + j, used - 1) * kPartial<D, NT>);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          const float g = k + j < used ? f[k + j] : 0.0f;
+          y0 = fmaf(v[j].x, g, y0);
+          y1 = fmaf(v[j].y, g, y1);
+        }
       }
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
       const long long row = r0 + r;
       const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
-      *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
+      *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * factor[r], y1 * factor[r]);
     }
     if (tid == 0) sk_reset(a.counters + tile_unit);
     __syncthreads();
@@ -367,7 +379,7 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   if (units > kCounterSlots) return 0;
   const long long chunk = nt ? std::max<long long>(kWaves, (units * tiles + 4 * cus - 1) / (4 * cus))
                              : std::max<long long>(8, (units * tiles + 2 * cus - 1) / (2 * cus));
-  const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, 128);
+  const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, kMostSplits);
   a->splits = static_cast<int>(splits);
   a->chunk = static_cast<int>((tiles + splits - 1) / splits);
   if (splits == 1) return 0;

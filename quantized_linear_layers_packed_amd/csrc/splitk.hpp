@@ -69,6 +69,16 @@ __device__ __forceinline__ void sk_store(int* p, int v) {
 __device__ __forceinline__ int sk_load(const int* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// Two floats at once (8-byte aligned).
+__device__ __forceinline__ void sk_store2(float* p, float a, float b) {
+  const unsigned long long v = __builtin_bit_cast(uint32_t, a) | (static_cast<unsigned long long>(__builtin_bit_cast(uint32_t, b)) << 32);
+  __hip_atomic_store(reinterpret_cast<unsigned long long*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 sk_load2(const float* p) {
+  const unsigned long long v =
+      __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__builtin_bit_cast(float, static_cast<uint32_t>(v)), __builtin_bit_cast(float, static_cast<uint32_t>(v >> 32)));
+}
 __device__ __forceinline__ void sk_drain_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Every thread of the workgroup calls this after storing its part of the
