@@ -422,7 +422,7 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  * zeros.
  *   Q device, tokens q_stride elements apart (a multiple of 8), Y device
  *   [tokens][q_heads][head_dim], both of dtype QLIN_F16 or QLIN_BF16; Y must not
- *   overlap Q.  scale: finite, > 0.
+ *   overlap Q.  scale: finite, > 0.  tokens * q_heads < 2^30 (EUNSUPPORTED).
  *   workspace: conventions at the top.
  * Codes enter the matrix instructions as exact fp16 integers and products are
  * summed in fp32; bf16 queries are scaled to fp16 by a power of two per row (as

@@ -242,6 +242,8 @@ qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qli
   QLIN_TRY(kv8_check_heads(fn, q_heads, a->c.heads));
   if (window < 0 || sinks < 0) return fail(QLIN_EINVAL, std::string(fn) + ": window and sinks must not be negative");
   if (sinks > 0 && window == 0) return fail(QLIN_EINVAL, std::string(fn) + ": sinks without a window");
+  if (static_cast<int64_t>(a->c.tokens) * q_heads >= (1 << 30))
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": tokens * q_heads must be below 2^30");
   a->q_heads = q_heads;
   a->group = q_heads / a->c.heads;
   a->window = window;

@@ -55,6 +55,22 @@ struct Kv8AppendArgs {
   uint16_t* Q_out;
 };
 
+// Division by a number known on the host: n / d for 0 <= n < 2^31, exactly
+// (d <= 65535: mul = ceil(2^(32 + shift) / d) with 2^(shift + 1) >= d fits 32
+// bits, and its error times n stays below 2^(32 + shift) / d).
+struct FastDiv {
+  uint32_t d = 1, mul = 0;
+  int shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t by) : d(by) {
+    while ((2u << shift) < by) ++shift;
+    mul = static_cast<uint32_t>(((uint64_t{1} << (32 + shift)) + by - 1) / by);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+  }
+};
+
 struct Kv8AttnArgs {
   Kv8View c;
   const uint16_t* Q;
@@ -65,6 +81,7 @@ struct Kv8AttnArgs {
   uint16_t* Y;
   // the split of long sequences (see kv8_attn.hip)
   int row_tiles, splits, chunk;
+  FastDiv by_group, by_heads, by_row_tiles, by_splits;
   int* counters;
   float* partials;
 };

@@ -47,7 +47,8 @@ namespace qlin {
 
 namespace {
 
-constexpr int kWaves = 4;
+// Waves of a workgroup: 8 where two waves' registers fit a SIMD, otherwise 4.
+constexpr int row_waves(int dim, int nt) { return dim * nt <= 128 ? 8 : 4; }
 constexpr int kMostSplits = 64;           // a lane each when they are joined
 // Maximum and sum over the four lanes q, q + 16, q + 32, q + 48.
 __device__ __forceinline__ float max_over_g(float v) {
@@ -98,28 +99,28 @@ constexpr size_t kPartial = 16 * NT * (D + 2);
 
 // Grid: splits x (sequence, row tile) x key/value heads, heads fastest.
 template <int D, int NT, bool BF16>
-__global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_rows_kernel(const Kv8AttnArgs a) {
-  constexpr int KU = D / 64, DT = D / 16;
+__global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void kv8_rows_kernel(const Kv8AttnArgs a) {
+  constexpr int KU = D / 64, DT = D / 16, kWaves = row_waves(D, NT);
   __shared__ __align__(16) float sums[kWaves][16][D + 4];
   __shared__ float refs[kWaves][16 * NT], weights[kWaves][16 * NT];
   __shared__ int flag;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, ql = lane & 15;
-  const int head = blockIdx.x % a.c.heads, unit = blockIdx.x / a.c.heads;
-  const int b = unit / a.row_tiles, split = blockIdx.y;
+  const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
+  const int b = a.by_row_tiles(unit), split = blockIdx.y;
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int P = 1 << a.c.log_page, G = a.group;
-  const long long rows = static_cast<long long>(seq.count) * G;
+  const int rows = seq.count * G;                             // below 2^30
   // row tiles past the grid are taken up in turn
-  for (long long r0 = static_cast<long long>(unit % a.row_tiles) * (16 * NT); r0 < rows; r0 += static_cast<long long>(a.row_tiles) * (16 * NT)) {
-    const int nrows = static_cast<int>(min(rows - r0, static_cast<long long>(16 * NT)));
-    const int p0 = seq.start + static_cast<int>(r0 / G), p1 = seq.start + static_cast<int>((r0 + nrows - 1) / G);
+  for (int r0 = (unit - b * a.row_tiles) * (16 * NT); r0 < rows; r0 += a.row_tiles * (16 * NT)) {
+    const int nrows = min(rows - r0, 16 * NT);
+    const int p0 = seq.start + a.by_group(r0), p1 = seq.start + a.by_group(r0 + nrows - 1);
     const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
     // row tiles beyond those planned for are not split: their partial results
     // would share workspace with the first ones'
-    const bool planned = r0 < static_cast<long long>(a.row_tiles) * (16 * NT);
-    const int per = planned ? max(a.chunk, (tiles.count + a.splits - 1) / a.splits) : max(tiles.count, 1);
-    const int used = max((tiles.count + per - 1) / per, 1);
-    if (split >= used) continue;
+    const bool planned = r0 < a.row_tiles * (16 * NT);
+    const int per = planned ? max(a.chunk, a.by_splits(tiles.count + a.splits - 1)) : max(tiles.count, 1);
+    if (split > 0 && split * per >= tiles.count) continue;
+    const int used = per >= tiles.count ? 1 : (tiles.count + per - 1) / per;
     const int x0 = split * per + wv, x1 = min(split * per + per, tiles.count);
 
     h8_t qf[NT][KU][2];
@@ -128,8 +129,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
     f32x4_t o[NT][DT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const long long r = r0 + min(16 * n + ql, nrows - 1);
-      const int t = static_cast<int>(r / G), h = head * G + static_cast<int>(r - static_cast<long long>(t) * G);
+      const int r = r0 + min(16 * n + ql, nrows - 1), t = a.by_group(r), h = head * G + r - t * G;
       load_rows<D, BF16>(a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(h) * D, g, qf[n], &cq[n]);
       cq[n] *= a.scale;
       pos[n] = seq.start + t;
@@ -297,8 +297,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
         }
         if (used == 1) {
           const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-          const long long row = r0 + r;
-          const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
+          const int row = r0 + r, t = a.by_group(row), h = head * G + row - t * G;
           *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
         } else {
           sk_store2(part + r * D + d, y0, y1);
@@ -340,8 +339,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
           y1 = fmaf(v[j].y, g, y1);
         }
       }
-      const long long row = r0 + r;
-      const int t = static_cast<int>(row / G), h = head * G + static_cast<int>(row - static_cast<long long>(t) * G);
+      const int row = r0 + r, t = a.by_group(row), h = head * G + row - t * G;
       *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * factor[r], y1 * factor[r]);
     }
     if (tid == 0) sk_reset(a.counters + tile_unit);
@@ -351,9 +349,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 && NT == 1 ? 2 : 1) void kv8_
 
 template <int D, int NT>
 void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits);
-  if (dtype == QLIN_BF16) hipLaunchKernelGGL((kv8_rows_kernel<D, NT, true>), grid, dim3(64 * kWaves), 0, stream, a);
-  else hipLaunchKernelGGL((kv8_rows_kernel<D, NT, false>), grid, dim3(64 * kWaves), 0, stream, a);
+  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * row_waves(D, NT));
+  if (dtype == QLIN_BF16) hipLaunchKernelGGL((kv8_rows_kernel<D, NT, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((kv8_rows_kernel<D, NT, false>), grid, block, 0, stream, a);
 }
 
 // 16-row column tiles per wave of the kernel for few rows, 0 for the kernel for
@@ -368,19 +366,24 @@ int rows_nt(const Kv8AttnArgs& a) {
 size_t kv8_attn_plan(Kv8AttnArgs* a) {
   const int nt = rows_nt(*a), cus = device_cus();
   const long long rows = static_cast<long long>(a->c.max_new) * a->group, tile_rows = nt ? 16 * nt : kv8_prompt_rows(a->c.dim);
-  const long long most = std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads));
+  const long long most = std::min(std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads)), 65535LL);
   a->row_tiles = static_cast<int>(std::min((rows + tile_rows - 1) / tile_rows, most));
   long long tiles = (static_cast<long long>(a->c.max_kv) + kTile - 1) / kTile;
   if (a->window > 0)
     tiles = std::min(tiles, (a->window + tile_rows / a->group) / kTile + 2 + (static_cast<long long>(a->sinks) + kTile - 1) / kTile);
   const long long units = static_cast<long long>(a->c.seqs) * a->row_tiles * a->c.heads;
+  a->by_group = FastDiv(a->group);
+  a->by_heads = FastDiv(a->c.heads);
+  a->by_row_tiles = FastDiv(a->row_tiles);
   a->splits = 1;
+  a->by_splits = FastDiv(1);
   a->chunk = static_cast<int>(tiles);
   if (units > kCounterSlots) return 0;
-  const long long chunk = nt ? std::max<long long>(kWaves, (units * tiles + 4 * cus - 1) / (4 * cus))
+  const long long chunk = nt ? std::max<long long>(row_waves(a->c.dim, nt), (units * tiles + cus - 1) / cus)
                              : std::max<long long>(8, (units * tiles + 2 * cus - 1) / (2 * cus));
   const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, kMostSplits);
   a->splits = static_cast<int>(splits);
+  a->by_splits = FastDiv(a->splits);
   a->chunk = static_cast<int>((tiles + splits - 1) / splits);
   if (splits == 1) return 0;
   const size_t partial = nt ? static_cast<size_t>(tile_rows) * (a->c.dim + 2) * sizeof(float) : kv8_prompt_partial(a->c.dim);

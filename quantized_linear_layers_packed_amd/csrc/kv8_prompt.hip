@@ -46,32 +46,30 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, D > 128 ? 1 : 2) void kv8_pro
   Tile16<D>* tile = reinterpret_cast<Tile16<D>*>(smem);    // two of them
   __shared__ int flag;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, h = lane >> 5, ql = lane & 31;
-  const int head = blockIdx.x % a.c.heads, unit = blockIdx.x / a.c.heads;
-  const int b = unit / a.row_tiles, split = blockIdx.y;
+  const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
+  const int b = a.by_row_tiles(unit), split = blockIdx.y;
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int P = 1 << a.c.log_page, G = a.group;
-  const long long rows = static_cast<long long>(seq.count) * G;
+  const int rows = seq.count * G;                             // below 2^30
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
   const int last_entry = (seq.len - 1) >> a.c.log_page;    // entries past it are not read
 
   // Row tiles from the last, which sees the most, to the first; row tiles past
   // the grid are taken up in turn.
-  for (long long r0 = static_cast<long long>(a.row_tiles - 1 - unit % a.row_tiles) * ROWS; r0 < rows;
-       r0 += static_cast<long long>(a.row_tiles) * ROWS) {
-    const int nrows = static_cast<int>(min(rows - r0, static_cast<long long>(ROWS)));
-    const int p0 = seq.start + static_cast<int>(r0 / G), p1 = seq.start + static_cast<int>((r0 + nrows - 1) / G);
+  for (int r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * ROWS; r0 < rows; r0 += a.row_tiles * ROWS) {
+    const int nrows = min(rows - r0, ROWS);
+    const int p0 = seq.start + a.by_group(r0), p1 = seq.start + a.by_group(r0 + nrows - 1);
     const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
     // row tiles beyond those planned for are not split: their partial results
     // would share workspace with the first ones'
-    const bool planned = r0 < static_cast<long long>(a.row_tiles) * ROWS;
-    const int per = planned ? max(a.chunk, (tiles.count + a.splits - 1) / a.splits) : max(tiles.count, 1);
-    const int used = max((tiles.count + per - 1) / per, 1);
-    if (split >= used) continue;
+    const bool planned = r0 < a.row_tiles * ROWS;
+    const int per = planned ? max(a.chunk, a.by_splits(tiles.count + a.splits - 1)) : max(tiles.count, 1);
+    if (split > 0 && split * per >= tiles.count) continue;
+    const int used = per >= tiles.count ? 1 : (tiles.count + per - 1) / per;
     const int x0 = split * per, x1 = min(x0 + per, tiles.count);
 
     // this lane's row
-    const long long r = r0 + min(32 * wv + ql, nrows - 1);
-    const int t = static_cast<int>(r / G), hq = head * G + static_cast<int>(r - static_cast<long long>(t) * G);
+    const int r = r0 + min(32 * wv + ql, nrows - 1), t = a.by_group(r), hq = head * G + r - t * G;
     const bool mine = 32 * wv + ql < nrows;
     const int pos = seq.start + t, low = a.window > 0 ? max(pos, 0) - a.window + 1 : 0;
     const int low_most = a.window > 0 ? max(p1, 0) - a.window + 1 : 0;
