@@ -81,6 +81,7 @@ struct Kv8AttnArgs {
   uint16_t* Y;
   // the split of long sequences (see kv8_attn.hip)
   int row_tiles, splits, chunk;
+  bool sorted;          // sequences in the order of their lengths
   FastDiv by_group, by_heads, by_row_tiles, by_splits;
   int* counters;
   float* partials;

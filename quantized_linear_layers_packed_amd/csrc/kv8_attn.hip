@@ -35,7 +35,6 @@
 // Bound by memory: 2 D bytes a token against 4 D 16 NT matrix flops.
 
 #include <algorithm>
-#include <cmath>
 
 #include "common.hpp"
 #include "device.hpp"
@@ -98,7 +97,11 @@ template <int D, int NT>
 constexpr size_t kPartial = 16 * NT * (D + 2);
 
 // Grid: splits x (sequence, row tile) x key/value heads, heads fastest.
-template <int D, int NT, bool BF16>
+// STREAM: V is read past the caches, which pays where a load covers whole 128-byte
+// lines (of pages of 128 tokens it takes every other half line): 131072 tokens of
+// 8 heads 54 -> 50 us, but 32 x 8192 tokens in pages of 128 99 -> 111 us.  K's
+// lines are shared by two loads each and stay cached.
+template <int D, int NT, bool BF16, bool STREAM>
 __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void kv8_rows_kernel(const Kv8AttnArgs a) {
   constexpr int KU = D / 64, DT = D / 16, kWaves = row_waves(D, NT);
   __shared__ __align__(16) float sums[kWaves][16][D + 4];
@@ -106,12 +109,13 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
   __shared__ int flag;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, ql = lane & 15;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
-  const int b = a.by_row_tiles(unit), split = blockIdx.y;
+  const int rank = a.by_row_tiles(unit), split = blockIdx.y;
+  const int b = !a.sorted ? rank : a.c.seqs <= 64 ? nth_longest<1>(a.c, rank) : nth_longest<kSortedSeqs / 64>(a.c, rank);
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int P = 1 << a.c.log_page, G = a.group;
   const int rows = seq.count * G;                             // below 2^30
   // row tiles past the grid are taken up in turn
-  for (int r0 = (unit - b * a.row_tiles) * (16 * NT); r0 < rows; r0 += a.row_tiles * (16 * NT)) {
+  for (int r0 = (unit - rank * a.row_tiles) * (16 * NT); r0 < rows; r0 += a.row_tiles * (16 * NT)) {
     const int nrows = min(rows - r0, 16 * NT);
     const int p0 = seq.start + a.by_group(r0), p1 = seq.start + a.by_group(r0 + nrows - 1);
     const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
@@ -146,7 +150,7 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
     const int last_entry = (seq.len - 1) >> a.c.log_page;       // entries past it are not read
     const int gk = (ql >> 2);
-    const int xl = x0 + (max(x1 - x0, 1) - 1) / kWaves * kWaves;   // this wave's last tile: loads past it repeat it
+    const int xl = x0 + (max(x1 - x0, 1) - 1) / kWaves * kWaves;   // this wave's last tile
     struct Pages { int k, v; };
     auto load_pages = [&](int x) {
       const int base = tiles[min(x, xl)] * kTile;
@@ -156,12 +160,16 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     uint4 kw[4][KU], vw[DT];
     float2 sc;
     bool held;
+    // Past the wave's last tile the loads are still issued (a branch around them
+    // would make the waits for the present tile wait for everything), all lanes at
+    // the pool's first bytes.
     auto load_k = [&](int x, const Pages& p) {
       const int base = tiles[min(x, xl)] * kTile;
       const size_t pk = valid(p.k) ? p.k : 0, pv = valid(p.v) ? p.v : 0;
       held = valid(p.v);
       sc = reinterpret_cast<const float2*>(a.c.scales)[pv * a.c.heads + head];   // not looked at unless held
-      const int8_t* src = a.c.k + (((pk * a.c.heads + head) << a.c.log_page) + ((base + 16 * gk) & (P - 1)) + (ql & 3)) * D + 16 * g;
+      const size_t at = (((pk * a.c.heads + head) << a.c.log_page) + ((base + 16 * gk) & (P - 1)) + (ql & 3)) * D + 16 * g;
+      const int8_t* src = a.c.k + (x <= xl ? at : 0);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -170,9 +178,15 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     auto load_v = [&](int x, const Pages& p) {
       const int base = tiles[min(x, xl)] * kTile;
       const size_t pv = valid(p.v) ? p.v : 0;
-      const int8_t* src = a.c.v + (((pv * a.c.heads + head) * D + ql) << a.c.log_page) + ((base + 16 * g) & (P - 1));
+      const size_t at = (((pv * a.c.heads + head) * D + ql) << a.c.log_page) + ((base + 16 * g) & (P - 1));
+      const int8_t* src = a.c.v + (x <= xl ? at : 0);
+      if constexpr (STREAM) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) vw[d] = *reinterpret_cast<const uint4*>(src + (static_cast<size_t>(16 * d) << a.c.log_page));
+        for (int d = 0; d < DT; ++d) vw[d] = load_stream16(src + (static_cast<size_t>(16 * d) << a.c.log_page));
+      } else {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) vw[d] = *reinterpret_cast<const uint4*>(src + (static_cast<size_t>(16 * d) << a.c.log_page));
+      }
     };
 
     if (x0 < x1) {
@@ -350,8 +364,10 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
 template <int D, int NT>
 void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * row_waves(D, NT));
-  if (dtype == QLIN_BF16) hipLaunchKernelGGL((kv8_rows_kernel<D, NT, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((kv8_rows_kernel<D, NT, false>), grid, block, 0, stream, a);
+  const bool bf16 = dtype == QLIN_BF16, stream_v = a.c.log_page < 7;
+  const auto fn = bf16 ? (stream_v ? kv8_rows_kernel<D, NT, true, true> : kv8_rows_kernel<D, NT, true, false>)
+                       : (stream_v ? kv8_rows_kernel<D, NT, false, true> : kv8_rows_kernel<D, NT, false, false>);
+  hipLaunchKernelGGL(fn, grid, block, 0, stream, a);
 }
 
 // 16-row column tiles per wave of the kernel for few rows, 0 for the kernel for
@@ -375,6 +391,8 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   a->by_group = FastDiv(a->group);
   a->by_heads = FastDiv(a->c.heads);
   a->by_row_tiles = FastDiv(a->row_tiles);
+  // more workgroups than run at once: the longest first
+  a->sorted = nt && a->c.seqs > 1 && a->c.seqs <= kSortedSeqs && units > cus;
   a->splits = 1;
   a->by_splits = FastDiv(1);
   a->chunk = static_cast<int>(tiles);
