@@ -80,7 +80,7 @@ struct Kv8AttnArgs {
   int window, sinks;    // window 0: none (sinks then 0)
   uint16_t* Y;
   // the split of long sequences (see kv8_attn.hip)
-  int row_tiles, splits, chunk;
+  int row_tiles, splits, chunk, waves;
   bool sorted;          // sequences in the order of their lengths
   FastDiv by_group, by_heads, by_row_tiles, by_splits;
   int* counters;

@@ -46,8 +46,8 @@ namespace qlin {
 
 namespace {
 
-// Waves of a workgroup: 8 where two waves' registers fit a SIMD, otherwise 4.
-constexpr int row_waves(int dim, int nt) { return dim * nt <= 128 ? 8 : 4; }
+// Waves of a SIMD that the registers allow.
+constexpr int row_occupancy(int dim, int nt) { return dim * nt <= 128 ? 2 : 1; }
 constexpr int kMostSplits = 64;           // a lane each when they are joined
 // Maximum and sum over the four lanes q, q + 16, q + 32, q + 48.
 __device__ __forceinline__ float max_over_g(float v) {
@@ -101,11 +101,11 @@ constexpr size_t kPartial = 16 * NT * (D + 2);
 // lines (of pages of 128 tokens it takes every other half line): 131072 tokens of
 // 8 heads 54 -> 50 us, but 32 x 8192 tokens in pages of 128 99 -> 111 us.  K's
 // lines are shared by two loads each and stay cached.
-template <int D, int NT, bool BF16, bool STREAM>
-__global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void kv8_rows_kernel(const Kv8AttnArgs a) {
-  constexpr int KU = D / 64, DT = D / 16, kWaves = row_waves(D, NT);
-  __shared__ __align__(16) float sums[kWaves][16][D + 4];
-  __shared__ float refs[kWaves][16 * NT], weights[kWaves][16 * NT];
+template <int D, int NT, int W, bool BF16, bool STREAM>
+__global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(const Kv8AttnArgs a) {
+  constexpr int KU = D / 64, DT = D / 16;
+  __shared__ __align__(16) float sums[W][16][D + 4];
+  __shared__ float refs[W][16 * NT], weights[W][16 * NT];
   __shared__ int flag;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, ql = lane & 15;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
     const int last_entry = (seq.len - 1) >> a.c.log_page;       // entries past it are not read
     const int gk = (ql >> 2);
-    const int xl = x0 + (max(x1 - x0, 1) - 1) / kWaves * kWaves;   // this wave's last tile
+    const int xl = x0 + (max(x1 - x0, 1) - 1) / W * W;   // this wave's last tile
     struct Pages { int k, v; };
     auto load_pages = [&](int x) {
       const int base = tiles[min(x, xl)] * kTile;
@@ -190,10 +190,10 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     };
 
     if (x0 < x1) {
-      Pages now = load_pages(x0), next = load_pages(x0 + kWaves);
+      Pages now = load_pages(x0), next = load_pages(x0 + W);
       load_k(x0, now);
       load_v(x0, now);
-      for (int x = x0; x < x1; x += kWaves) {
+      for (int x = x0; x < x1; x += W) {
         const int base = tiles[x] * kTile, j0 = base + 16 * g;
         const bool here = held;
         const float2 s = sc;
@@ -213,8 +213,8 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
           }
         }
         const Pages coming = next;
-        next = load_pages(x + 2 * kWaves);
-        load_k(x + kWaves, coming);
+        next = load_pages(x + 2 * W);
+        load_k(x + W, coming);
 
         // every position of the tile visible to every row, and every page there
         const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && !__any(!here);
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
             o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[n][1], o[n][d], 0, 0, 0);
           }
         }
-        load_v(x + kWaves, coming);
+        load_v(x + W, coming);
       }
     }
 
@@ -291,20 +291,20 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     for (int n = 0; n < NT; ++n) {
       float top = refs[0][16 * n + ql];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, refs[w][16 * n + ql]);
+      for (int w = 1; w < W; ++w) top = fmaxf(top, refs[w][16 * n + ql]);
       const float f = exp2f(m[n] - top);
 #pragma unroll
       for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(&sums[wv][ql][16 * d + 4 * g]) = o[n][d] * f;
       __syncthreads();
-      for (int i = tid; i < 16 * D / 2; i += 64 * kWaves) {
+      for (int i = tid; i < 16 * D / 2; i += 64 * W) {
         const int rr = i / (D / 2), d = 2 * (i - rr * (D / 2)), r = 16 * n + rr;
         if (r >= nrows) break;
         float ref = refs[0][r];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) ref = fmaxf(ref, refs[w][r]);
+        for (int w = 1; w < W; ++w) ref = fmaxf(ref, refs[w][r]);
         float total = 0.0f, y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
           total = fmaf(weights[w][r], exp2f(refs[w][r] - ref), total);
           y0 += sums[w][rr][d];
           y1 += sums[w][rr][d + 1];
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
     const float* first = a.partials + static_cast<size_t>(tile_unit) * a.splits * kPartial<D, NT>;
     float* weigh = &sums[0][0][0];                            // [row][split], the rows' factors after them
     float* factor = weigh + 16 * NT * kMostSplits;
-    for (int r = wv; r < nrows; r += kWaves) {
+    for (int r = wv; r < nrows; r += W) {
       const float2 mine = lane < used ? sk_load2(first + lane * kPartial<D, NT> + 16 * NT * D + 2 * r) : make_float2(kNone, 0.0f);
       const float f = __builtin_amdgcn_exp2f(mine.x - wave_max(mine.x));
       weigh[r * kMostSplits + lane] = f;
@@ -336,7 +336,7 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
       if (lane == 0) factor[r] = total == 0.0f ? 0.0f : 1.0f / total;
     }
     __syncthreads();
-    for (int i = tid; i < nrows * (D / 2); i += 64 * kWaves) {
+    for (int i = tid; i < nrows * (D / 2); i += 64 * W) {
       const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
       const float* src = first + r * D + d;
       const float* f = weigh + r * kMostSplits;
@@ -361,12 +361,12 @@ __global__ __launch_bounds__(64 * row_waves(D, NT), row_waves(D, NT) / 4) void k
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int W>
 void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * row_waves(D, NT));
+  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * W);
   const bool bf16 = dtype == QLIN_BF16, stream_v = a.c.log_page < 7;
-  const auto fn = bf16 ? (stream_v ? kv8_rows_kernel<D, NT, true, true> : kv8_rows_kernel<D, NT, true, false>)
-                       : (stream_v ? kv8_rows_kernel<D, NT, false, true> : kv8_rows_kernel<D, NT, false, false>);
+  const auto fn = bf16 ? (stream_v ? kv8_rows_kernel<D, NT, W, true, true> : kv8_rows_kernel<D, NT, W, true, false>)
+                       : (stream_v ? kv8_rows_kernel<D, NT, W, false, true> : kv8_rows_kernel<D, NT, W, false, false>);
   hipLaunchKernelGGL(fn, grid, block, 0, stream, a);
 }
 
@@ -375,6 +375,19 @@ void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
 int rows_nt(const Kv8AttnArgs& a) {
   const long long rows = static_cast<long long>(a.c.max_new) * a.group;
   return rows <= 16 ? 1 : rows <= 32 && a.c.dim <= 128 ? 2 : 0;
+}
+
+// Waves of a workgroup.  With 4, two workgroups share a compute unit and one's
+// beginning and end hide behind the other's tiles: many short sequences are
+// faster (200 x 512 tokens of 8 heads 78 -> 52 us, one of 1024 11.5 -> 9.5 us).
+// With 8, long sequences that leave at most two workgroups to a compute unit end
+// together more nearly (64 ragged ones of up to 8192: 99 -> 86 us) and fewer
+// splits have to be joined.  Two column tiles of narrow heads (draft
+// verification) have no short form that pays: 27 against 23 us for 32 windows of
+// 4096.
+int rows_waves(const Kv8AttnArgs& a, int nt, long long units, long long tiles, int cus) {
+  if (row_occupancy(a.c.dim, nt) == 1) return 4;
+  return nt == 2 || (tiles >= 64 && units * tiles >= 64LL * cus && units <= 2LL * cus) ? 8 : 4;
 }
 
 }  // namespace
@@ -391,14 +404,15 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   a->by_group = FastDiv(a->group);
   a->by_heads = FastDiv(a->c.heads);
   a->by_row_tiles = FastDiv(a->row_tiles);
+  a->waves = nt ? rows_waves(*a, nt, units, tiles, cus) : 0;
   // more workgroups than run at once: the longest first
   a->sorted = nt && a->c.seqs > 1 && a->c.seqs <= kSortedSeqs && units > cus;
   a->splits = 1;
   a->by_splits = FastDiv(1);
   a->chunk = static_cast<int>(tiles);
   if (units > kCounterSlots) return 0;
-  const long long chunk = nt ? std::max<long long>(row_waves(a->c.dim, nt), (units * tiles + cus - 1) / cus)
-                             : std::max<long long>(8, (units * tiles + 2 * cus - 1) / (2 * cus));
+  const long long share = (units * tiles + cus - 1) / cus;    // tiles per compute unit
+  const long long chunk = nt ? std::max<long long>(a->waves, share) : std::max<long long>(8, (share + 1) / 2);
   const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, kMostSplits);
   a->splits = static_cast<int>(splits);
   a->by_splits = FastDiv(a->splits);
@@ -414,10 +428,17 @@ void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
     kv8_prompt_launch(a, dtype, stream);
     return;
   }
+  const bool wide = a.waves == 8;
   switch (a.c.dim) {
-    case 64: nt == 1 ? rows_launch<64, 1>(a, dtype, stream) : rows_launch<64, 2>(a, dtype, stream); break;
-    case 128: nt == 1 ? rows_launch<128, 1>(a, dtype, stream) : rows_launch<128, 2>(a, dtype, stream); break;
-    default: rows_launch<256, 1>(a, dtype, stream); break;
+    case 64:
+      if (nt == 2) rows_launch<64, 2, 8>(a, dtype, stream);
+      else wide ? rows_launch<64, 1, 8>(a, dtype, stream) : rows_launch<64, 1, 4>(a, dtype, stream);
+      break;
+    case 128:
+      if (nt == 2) rows_launch<128, 2, 4>(a, dtype, stream);
+      else wide ? rows_launch<128, 1, 8>(a, dtype, stream) : rows_launch<128, 1, 4>(a, dtype, stream);
+      break;
+    default: rows_launch<256, 1, 4>(a, dtype, stream); break;
   }
 }
 
