@@ -12,6 +12,8 @@ constexpr float kSlack = 8.0f;                 // scores may exceed the row's re
 constexpr float kNone = -1.0e30f;              // reference of a row that has seen nothing
 constexpr float kLeastScale = 7.8886091e-31f;  // 2^-100: smaller value scales (0 among them) count as that
 
+constexpr float kLeastFactor = 1.0e-30f;       // smaller score factors (0 among them) count as that: no score changes
+
 // 8 codes (two words) as 8 fp16 integers, in order: byte + 128 into the low
 // mantissa of 1024, minus 1152.
 __device__ __forceinline__ h8_t codes_f16(uint32_t w0, uint32_t w1) {

@@ -11,8 +11,7 @@
 //   O^T += V^T P tokens, the weights of tokens 8 h .. 8 h + 7 for row q: the B
 //                operand of the second product as it stands, because K's rows are
 //                fed in the order that makes it so.
-// A run of 16 tokens lies in one page: its two scales are the same for the whole
-// wave and come as scalars.
+// A run of 16 tokens lies in one page: its two scales are the same for every lane.
 
 #include <algorithm>
 
@@ -26,8 +25,19 @@ namespace qlin {
 
 namespace {
 
+// Waves of a workgroup, and of a SIMD.  A code is converted once per workgroup, so
+// more waves convert less; heads of 256 dimensions fill the registers with one
+// wave per SIMD, those of 64 leave room for three.
 template <int D>
 constexpr int kPromptWaves = D == 128 ? 8 : 4;
+template <int D>
+constexpr int kPromptOccupancy = D > 128 ? 1 : D > 64 ? 2 : 3;
+
+// A run of 16 tokens of a tile: its key scale, log2 and reciprocal of its value
+// scale.
+struct Run {
+  float key, lv, iv, unused;
+};
 
 // fp16 tiles in LDS, rows padded by 16 bytes so that 16 lanes reading 16 bytes
 // each of consecutive rows hit every bank once.
@@ -35,10 +45,28 @@ template <int D>
 struct Tile16 {
   _Float16 k[kTile][D + 8];
   _Float16 v[D][kTile + 8];
+  Run run[4];
+  uint32_t held;                                            // bit s: run s has a page
 };
 
+// Schedules N products whose A operands come from LDS so that a product's operand
+// is on its way four products ahead (the compiler alone asks for it one product
+// ahead and waits: 2-3 % slower), and ends the scheduling region.
+template <int N>
+__device__ __forceinline__ void lookahead() {
+  constexpr int AHEAD = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);     // LDS reads
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);         // a matrix product
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int D, bool BF16>
-__global__ __launch_bounds__(64 * kPromptWaves<D>, D > 128 ? 1 : 2) void kv8_prompt_kernel(const Kv8AttnArgs a) {
+__global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8_prompt_kernel(const Kv8AttnArgs a) {
   constexpr int W = kPromptWaves<D>, NT = 64 * W, ROWS = 32 * W, DT = D / 32, KS = D / 16;
   constexpr int NL = D * kTile / 16 / NT;                  // 16-byte pieces of K (and of V) per thread and tile
   constexpr int SLOT = W * 64 * (16 * DT + 2);             // floats of a split's partial result
@@ -98,39 +126,44 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, D > 128 ? 1 : 2) void kv8_pro
       for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
     float m = kNone, l = 0.0f;
 
-    auto valid = [&](int page) { return static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages); };
-    auto page_at = [&](int position) { return table[min(position >> a.c.log_page, last_entry)]; };
-
-    // Codes of a tile on their way to LDS, the page entries of the tile after it,
-    // and the scales of the tile's four runs of 16 tokens (lane % 4).
+    // Loads of a tile.  A thread's place in the tile's pages is fixed (but for where
+    // the tile lies in pages longer than it): its K row `token` and its V piece (16
+    // tokens, number tid % 4) each have one page entry, the latter also that of the
+    // run of tokens whose scales the thread takes.  Its n-th pieces lie STEP tokens
+    // (a multiple of 16, so `token` stays in the same place of a page) and NT / 4
+    // dimensions further.
+    constexpr int STEP = NT / (D / 16);
+    const size_t block_bytes = static_cast<size_t>(D) << a.c.log_page;
+    const int token = tid / (D / 16);
+    const int8_t* kplace = a.c.k + (token & (P - 1)) * D + 16 * (tid % (D / 16));
+    const int8_t* vplace = a.c.v + (static_cast<size_t>(tid / 4) << a.c.log_page) + ((16 * (tid % 4)) & (P - 1));
+    const int kentry = token >> a.c.log_page, ventry = (16 * (tid % 4)) >> a.c.log_page;
     uint4 kw[NL], vw[NL];
-    int kpage[NL], vpage[NL], spage;
-    float run_k, run_lv, run_iv;
-    bool run_held;
-    auto load_pages = [&](int x) {
-      const int base = tiles[min(x, x1 - 1)] * kTile;
-#pragma unroll
-      for (int n = 0; n < NL; ++n) {
-        kpage[n] = page_at(base + (tid + n * NT) / (D / 16));
-        vpage[n] = page_at(base + 16 * ((tid + n * NT) % 4));
-      }
-      spage = page_at(base + 16 * (lane & 3));
-    };
+    int kpage[NL], vpage;
     float2 scale2;
-    auto load_codes = [&](int x) {
-      const int base = tiles[min(x, x1 - 1)] * kTile;
-#pragma unroll
-      for (int n = 0; n < NL; ++n) {
-        const int i = tid + n * NT, token = i / (D / 16), c = i % (D / 16);
-        const size_t pk = (static_cast<size_t>(valid(kpage[n]) ? kpage[n] : 0) * a.c.heads + head) << a.c.log_page;
-        kw[n] = *reinterpret_cast<const uint4*>(a.c.k + (pk + ((base + token) & (P - 1))) * D + 16 * c);
-        const size_t pv = (static_cast<size_t>(valid(vpage[n]) ? vpage[n] : 0) * a.c.heads + head) * D + i / 4;
-        vw[n] = *reinterpret_cast<const uint4*>(a.c.v + (pv << a.c.log_page) + ((base + 16 * (i % 4)) & (P - 1)));
-      }
-      run_held = valid(spage);
-      scale2 = reinterpret_cast<const float2*>(a.c.scales)[static_cast<size_t>(run_held ? spage : 0) * a.c.heads + head];
+    bool held_next;
+    auto block_of = [&](int page) {                         // pages that are not there: any other
+      return static_cast<uint32_t>(static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages) ? page : 0) * a.c.heads + head;
     };
-    auto put_codes = [&](Tile16<D>& to) {
+    auto load_pages = [&](int x) {
+      const int entry = (tiles[min(x, x1 - 1)] * kTile) >> a.c.log_page;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) kpage[n] = table[static_cast<unsigned>(min(entry + kentry + ((n * STEP) >> a.c.log_page), last_entry))];
+      vpage = table[static_cast<unsigned>(min(entry + ventry, last_entry))];
+    };
+    auto load_codes = [&](int x) {
+      const int within = (tiles[min(x, x1 - 1)] * kTile) & (P - 1);
+#pragma unroll
+      for (int n = 0; n < NL; ++n)
+        kw[n] = *reinterpret_cast<const uint4*>(kplace + block_of(kpage[n]) * block_bytes + (within + ((n * STEP) & (P - 1))) * D);
+      const uint32_t block = block_of(vpage);
+#pragma unroll
+      for (int n = 0; n < NL; ++n)
+        vw[n] = *reinterpret_cast<const uint4*>(vplace + block * block_bytes + within + (static_cast<size_t>(n * (NT / 4)) << a.c.log_page));
+      scale2 = reinterpret_cast<const float2*>(a.c.scales)[block];
+      held_next = static_cast<unsigned>(vpage) < static_cast<unsigned>(a.c.pages);
+    };
+    auto put_codes = [&](Tile16<D>& to) __attribute__((always_inline)) {
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         const int i = tid + n * NT, token = i / (D / 16), c = i % (D / 16);
@@ -139,10 +172,12 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, D > 128 ? 1 : 2) void kv8_pro
         *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4)]) = codes_f16(vw[n].x, vw[n].y);
         *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4) + 8]) = codes_f16(vw[n].z, vw[n].w);
       }
-      const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;       // NaN stays
-      run_k = scale2.x;
-      run_lv = __log2f(vs);
-      run_iv = 1.0f / vs;
+      if (tid < 4) {
+        const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
+        to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs), 0.0f};
+      }
+      const uint32_t held = static_cast<uint32_t>(__ballot(held_next)) & 15u;  // lanes 0 .. 3 of wave 0: the four runs
+      if (tid == 0) to.held = held;
     };
 
     if (x0 < x1) {
@@ -150,112 +185,112 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, D > 128 ? 1 : 2) void kv8_pro
       load_codes(x0);
       load_pages(x0 + 1);
       put_codes(tile[0]);
-    }
-    // K row that this lane feeds to row `lane % 32` of a 32-token product
-    const int krow = 16 * (ql >> 4) + 8 * ((ql >> 2) & 1) + 4 * ((ql >> 3) & 1) + (ql & 3);
-    for (int x = x0; x < x1; ++x) {
-      const Tile16<D>& now = tile[(x - x0) & 1];
-      const int base = tiles[x] * kTile;
-      // the runs' scales as scalars (lane s holds run s)
-      float ks[4], lv[4], iv[4];
-      bool held[4], all_held = true;
+      // (the loop inside this block, so that its waits know that the queries are there)
+      // K row that this lane feeds to row `lane % 32` of a 32-token product
+      const int krow = 16 * (ql >> 4) + 8 * ((ql >> 2) & 1) + 4 * ((ql >> 3) & 1) + (ql & 3);
+      for (int x = x0; x < x1; ++x) {
+        const Tile16<D>& now = tile[(x - x0) & 1];
+        const int base = tiles[x] * kTile;
+        load_codes(x + 1);
+        load_pages(x + 2);
+        __syncthreads();                                      // the tile is complete, and the other one is free
+        f32x16_t st[2];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        ks[s] = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(run_k), s));
-        lv[s] = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(run_lv), s));
-        iv[s] = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(run_iv), s));
-        held[s] = __builtin_amdgcn_readlane(run_held, s) != 0;
-        all_held = all_held && held[s];
-      }
-      load_codes(x + 1);
-      load_pages(x + 2);
-      __syncthreads();                                      // the tile is complete, and the other one is free
-
-      f32x16_t st[2];
+        for (int T = 0; T < 2; ++T) {
 #pragma unroll
-      for (int T = 0; T < 2; ++T) {
+          for (int i = 0; i < 16; ++i) st[T][i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st[T][i] = 0.0f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          st[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.k[32 * T + krow][16 * s + 8 * h]), qf[s],
-                                                         st[T], 0, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && all_held;
-      uint32_t seen[4];                                     // bit i of run s: this lane's token i
-      if (!full) {
+          for (int s = 0; s < KS; ++s)
+            st[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.k[32 * T + krow][16 * s + 8 * h]), qf[s],
+                                                           st[T], 0, 0, 0);
+        }
+        if constexpr (D > 64) lookahead<2 * KS>();            // (narrow heads have no registers for it)
+        else __builtin_amdgcn_sched_barrier(0);
+        float c[4], lv[4], iv[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          seen[s] = visible_bits<8>(base + 16 * s + 8 * h, pos, low, a.sinks, held[s]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : -INFINITY;
+          const Run run = now.run[s];
+          c[s] = run.key * cq;
+          lv[s] = run.lv;
+          iv[s] = run.iv;
         }
-      }
-      // run s: values st[s / 2][8 (s % 2) .. + 7]
-      float c[4], top = kNone;
+        const uint32_t held = __builtin_amdgcn_readfirstlane(now.held);
+        const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && held == 15u;
+        uint32_t seen[4];                                     // bit i of run s: this lane's token i
+        if (!full) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        c[s] = ks[s] * cq;
-        float mx = st[s >> 1][8 * (s & 1)];
+          for (int s = 0; s < 4; ++s) {
+            seen[s] = visible_bits<8>(base + 16 * s + 8 * h, pos, low, a.sinks, (held >> s) & 1u);
 #pragma unroll
-        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, st[s >> 1][8 * (s & 1) + i]);
-        top = fmaxf(top, fmaf(mx, c[s], lv[s]));
-      }
-      if (__any(top > m + kSlack)) {
-        const float high = fmaxf(top, __shfl_xor(top, 32, 64)), was = m;
-        m = high > was + kSlack ? high : was;               // by the row's own scores alone
-        const float f = __builtin_amdgcn_exp2f(was - m);
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] *= f;
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float shift = lv[s] - m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = 8 * (s & 1) + i;
-          st[s >> 1][k] = __builtin_amdgcn_exp2f(fmaf(st[s >> 1][k], c[s], shift));
+            for (int i = 0; i < 8; ++i)
+              st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : -INFINITY;
+          }
         }
-      }
-      if (!full) {                                          // scales of hidden pages may be anything, NaN among it
+        // run s: values st[s / 2][8 (s % 2) .. + 7]
+        float top = kNone;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          iv[s] = seen[s] != 0 ? iv[s] : 0.0f;
+          float mx = st[s >> 1][8 * (s & 1)];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : 0.0f;
+          for (int i = 1; i < 8; ++i) mx = fmaxf(mx, st[s >> 1][8 * (s & 1) + i]);
+          top = fmaxf(top, fmaf(mx, c[s], lv[s]));
         }
-      }
-      h8_t pf[4];
+        if (__any(top > m + kSlack)) {
+          const float high = fmaxf(top, __shfl_xor(top, 32, 64)), was = m;
+          m = high > was + kSlack ? high : was;               // by the row's own scores alone
+          const float f = __builtin_amdgcn_exp2f(was - m);
+          l *= f;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        float part = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = st[s >> 1][8 * (s & 1) + i];
-          part += p;
-          pf[s][i] = static_cast<_Float16>(p);
+          for (int d = 0; d < DT; ++d) o[d] *= f;
         }
-        l = fmaf(part, iv[s], l);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float shift = lv[s] - m;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = 8 * (s & 1) + i;
+            st[s >> 1][k] = __builtin_amdgcn_exp2f(fmaf(st[s >> 1][k], c[s], shift));
+          }
+        }
+        if (!full) {                                          // scales of hidden pages may be anything, NaN among it
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            iv[s] = seen[s] != 0 ? iv[s] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : 0.0f;
+          }
+        }
+        h8_t pf[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          float part = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float p = st[s >> 1][8 * (s & 1) + i];
+            part += p;
+            pf[s][i] = static_cast<_Float16>(p);
+          }
+          l = fmaf(part, iv[s], l);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.v[32 * d + ql][16 * s + 8 * h]), pf[s],
+                                                          o[d], 0, 0, 0);
+        put_codes(tile[(x - x0 + 1) & 1]);
+        if constexpr (D > 64) lookahead<4 * DT>();
       }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.v[32 * d + ql][16 * s + 8 * h]), pf[s],
-                                                        o[d], 0, 0, 0);
-      put_codes(tile[(x - x0 + 1) & 1]);
     }
     l += __shfl_xor(l, 32, 64);
 
     if (used > 1) {
       // every value of the partial result at its register's and lane's own place
-      float* slots = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * SLOT + wv * 64 * (16 * DT + 2) + lane;
-      asm volatile("" : "+v"(slots));                       // its 16 DT offsets are not to be held through the loop
+      int place = wv * 64 * (16 * DT + 2) + lane;
+      asm volatile("" : "+v"(place));                       // its 16 DT addresses are not to be held through the loop
+      float* slots = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * SLOT + place;
       float* part = slots + static_cast<size_t>(split) * SLOT;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
