@@ -94,8 +94,10 @@ void kv8_gather_launch(const Kv8View& c, uint16_t* K, uint16_t* V, int dtype, hi
 // call needs no workspace).
 size_t kv8_attn_plan(Kv8AttnArgs* a);
 void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream);
-// The kernel for many rows: rows of a workgroup, bytes of a split's partial result.
+// The kernel for many rows: rows of a workgroup, workgroups that share a compute
+// unit, bytes of a split's partial result.
 int kv8_prompt_rows(int dim);
+int kv8_prompt_resident(int dim);
 size_t kv8_prompt_partial(int dim);
 void kv8_prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream);
 

@@ -49,16 +49,6 @@ namespace {
 // Waves of a SIMD that the registers allow.
 constexpr int row_occupancy(int dim, int nt) { return dim * nt <= 128 ? 2 : 1; }
 constexpr int kMostSplits = 64;           // a lane each when they are joined
-// Maximum and sum over the four lanes q, q + 16, q + 32, q + 48.
-__device__ __forceinline__ float max_over_g(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
-}
-__device__ __forceinline__ float sum_over_g(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
-}
-
 // 16 NT query rows as B operands: lane (q, g), slice (u, e) holds dimensions
 // 64 u + 16 g + 8 e .. + 7 of row q.  bf16 rows are scaled by a power of two into
 // fp16's range; *mul is what undoes it.
@@ -81,9 +71,7 @@ __device__ __forceinline__ void load_rows(const uint16_t* row, int g, h8_t (&q)[
     for (int u = 0; u < D / 64; ++u)
 #pragma unroll
       for (int e = 0; e < 2; ++e) most = max(most, chunk_most(w[u][e]));
-    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 16, 64)));
-    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 32, 64)));
-    const int e14 = row_exponent(most);
+    const int e14 = row_exponent(most_over_g(most));
     *mul = ldexpf(1.0f, e14);
 #pragma unroll
     for (int u = 0; u < D / 64; ++u)
@@ -412,12 +400,24 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   a->chunk = static_cast<int>(tiles);
   if (units > kCounterSlots) return 0;
   const long long share = (units * tiles + cus - 1) / cus;    // tiles per compute unit
-  const long long chunk = nt ? std::max<long long>(a->waves, share) : std::max<long long>(8, (share + 1) / 2);
-  const long long splits = std::min<long long>((tiles + chunk - 1) / chunk, kMostSplits);
+  long long splits = 1;
+  if (nt) {
+    splits = (tiles + std::max<long long>(a->waves, share) - 1) / std::max<long long>(a->waves, share);
+  } else {
+    // rounds of the workgroups over the compute units, times a workgroup's tiles and
+    // what its beginning and end (and joining splits) cost in tiles
+    const long long slots = static_cast<long long>(cus) * kv8_prompt_resident(a->c.dim);
+    long long best = -1;
+    for (long long n = 1; n <= kMostSplits && n <= std::max<long long>(tiles / 2, 1); ++n) {
+      const long long cost = ((units * n + slots - 1) / slots) * ((tiles + n - 1) / n + (n > 1 ? 6 : 3));
+      if (best < 0 || cost < best) best = cost, splits = n;
+    }
+  }
+  splits = std::min<long long>(splits, kMostSplits);
   a->splits = static_cast<int>(splits);
   a->by_splits = FastDiv(a->splits);
   a->chunk = static_cast<int>((tiles + splits - 1) / splits);
-  if (splits == 1) return 0;
+  if (a->splits == 1) return 0;
   const size_t partial = nt ? static_cast<size_t>(tile_rows) * (a->c.dim + 2) * sizeof(float) : kv8_prompt_partial(a->c.dim);
   return static_cast<size_t>(units) * splits * partial;
 }

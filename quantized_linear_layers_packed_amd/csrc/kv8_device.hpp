@@ -31,6 +31,43 @@ __device__ __forceinline__ h8_t codes_f16(uint32_t w0, uint32_t w1) {
   return r;
 }
 
+// Exchanges between lanes 32 (or 16 and 32) apart on the VALU: both operands of a
+// swap hold v, so that afterwards one holds the lower partner's value in both
+// lanes and the other the upper partner's.
+__device__ __forceinline__ float2 pair_over_32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(bitcast<uint32_t>(v), bitcast<uint32_t>(v), false, false);
+  return make_float2(bitcast<float>(static_cast<uint32_t>(r[0])), bitcast<float>(static_cast<uint32_t>(r[1])));
+}
+__device__ __forceinline__ float2 pair_over_16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(bitcast<uint32_t>(v), bitcast<uint32_t>(v), false, false);
+  return make_float2(bitcast<float>(static_cast<uint32_t>(r[0])), bitcast<float>(static_cast<uint32_t>(r[1])));
+}
+__device__ __forceinline__ float max_over_32(float v) {
+  const float2 p = pair_over_32(v);
+  return fmaxf(p.x, p.y);
+}
+__device__ __forceinline__ float sum_over_32(float v) {
+  const float2 p = pair_over_32(v);
+  return p.x + p.y;
+}
+__device__ __forceinline__ uint32_t most_over_32(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(static_cast<uint32_t>(r[0]), static_cast<uint32_t>(r[1]));
+}
+// Over the four lanes q, q + 16, q + 32, q + 48.
+__device__ __forceinline__ float max_over_g(float v) {
+  const float2 p = pair_over_16(v);
+  return max_over_32(fmaxf(p.x, p.y));
+}
+__device__ __forceinline__ float sum_over_g(float v) {
+  const float2 p = pair_over_16(v);
+  return sum_over_32(p.x + p.y);
+}
+__device__ __forceinline__ uint32_t most_over_g(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return most_over_32(max(static_cast<uint32_t>(r[0]), static_cast<uint32_t>(r[1])));
+}
+
 // The tiles of 64 positions that the rows at positions p0 .. p1 see: those of the
 // first tokens and those from the start of the window of p0.
 struct Kv8Tiles {

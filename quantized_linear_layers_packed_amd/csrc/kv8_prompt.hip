@@ -35,14 +35,14 @@ constexpr int kPromptOccupancy = D > 128 ? 1 : D > 64 ? 2 : 3;
 
 // A run of 16 tokens of a tile: its key scale, log2 and reciprocal of its value
 // scale.
-struct Run {
-  float key, lv, iv, unused;
+struct alignas(16) Run {
+  float key, lv, iv;
 };
 
 // fp16 tiles in LDS, rows padded by 16 bytes so that 16 lanes reading 16 bytes
 // each of consecutive rows hit every bank once.
 template <int D>
-struct Tile16 {
+struct alignas(16) Tile16 {
   _Float16 k[kTile][D + 8];
   _Float16 v[D][kTile + 8];
   Run run[4];
@@ -104,13 +104,14 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     h8_t qf[KS];                                            // slice s: dimensions 16 s + 8 h .. + 7
     float cq = a.scale;
     {
-      const uint16_t* row = a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(hq) * D + 8 * h;
+      int again = tid;
+      asm volatile("" : "+v"(again));                       // (nothing of the address to be held for the next rows)
+      const uint16_t* row = a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(hq) * D + ((again & 32) >> 2);
       if constexpr (BF16) {
         uint32_t most = 0;
 #pragma unroll
         for (int s = 0; s < KS; ++s) most = max(most, chunk_most(*reinterpret_cast<const uint4*>(row + 16 * s)));
-        most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), 32, 64)));
-        const int e = row_exponent(most);
+        const int e = row_exponent(most_over_32(most));
         cq *= ldexpf(1.0f, e);
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[s] = chunk_f16(*reinterpret_cast<const uint4*>(row + 16 * s), e);
@@ -135,8 +136,8 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     constexpr int STEP = NT / (D / 16);
     const size_t block_bytes = static_cast<size_t>(D) << a.c.log_page;
     const int token = tid / (D / 16);
-    const int8_t* kplace = a.c.k + (token & (P - 1)) * D + 16 * (tid % (D / 16));
-    const int8_t* vplace = a.c.v + (static_cast<size_t>(tid / 4) << a.c.log_page) + ((16 * (tid % 4)) & (P - 1));
+    const uint32_t kplace = (token & (P - 1)) * D + 16 * (tid % (D / 16));
+    const uint32_t vplace = ((tid / 4) << a.c.log_page) + ((16 * (tid % 4)) & (P - 1));
     const int kentry = token >> a.c.log_page, ventry = (16 * (tid % 4)) >> a.c.log_page;
     uint4 kw[NL], vw[NL];
     int kpage[NL], vpage;
@@ -155,11 +156,11 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
       const int within = (tiles[min(x, x1 - 1)] * kTile) & (P - 1);
 #pragma unroll
       for (int n = 0; n < NL; ++n)
-        kw[n] = *reinterpret_cast<const uint4*>(kplace + block_of(kpage[n]) * block_bytes + (within + ((n * STEP) & (P - 1))) * D);
+        kw[n] = *reinterpret_cast<const uint4*>(a.c.k + (block_of(kpage[n]) * block_bytes + (kplace + (within + ((n * STEP) & (P - 1))) * D)));
       const uint32_t block = block_of(vpage);
 #pragma unroll
       for (int n = 0; n < NL; ++n)
-        vw[n] = *reinterpret_cast<const uint4*>(vplace + block * block_bytes + within + (static_cast<size_t>(n * (NT / 4)) << a.c.log_page));
+        vw[n] = *reinterpret_cast<const uint4*>(a.c.v + (block * block_bytes + (vplace + within + ((n * (NT / 4)) << a.c.log_page))));
       scale2 = reinterpret_cast<const float2*>(a.c.scales)[block];
       held_next = static_cast<unsigned>(vpage) < static_cast<unsigned>(a.c.pages);
     };
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
       }
       if (tid < 4) {
         const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
-        to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs), 0.0f};
+        to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs)};
       }
       const uint32_t held = static_cast<uint32_t>(__ballot(held_next)) & 15u;  // lanes 0 .. 3 of wave 0: the four runs
       if (tid == 0) to.held = held;
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
           top = fmaxf(top, fmaf(mx, c[s], lv[s]));
         }
         if (__any(top > m + kSlack)) {
-          const float high = fmaxf(top, __shfl_xor(top, 32, 64)), was = m;
+          const float high = max_over_32(top), was = m;
           m = high > was + kSlack ? high : was;               // by the row's own scores alone
           const float f = __builtin_amdgcn_exp2f(was - m);
           l *= f;
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
         if constexpr (D > 64) lookahead<4 * DT>();
       }
     }
-    l += __shfl_xor(l, 32, 64);
+    l = sum_over_32(l);
 
     if (used > 1) {
       // every value of the partial result at its register's and lane's own place
@@ -321,7 +322,9 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     }
     if (mine) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + 4 * h;
+      int again = tid;
+      asm volatile("" : "+v"(again));                       // (nothing of the address to be held through the loop)
+      uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + ((again & 32) >> 3);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -344,6 +347,11 @@ void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
 }  // namespace
 
 int kv8_prompt_rows(int dim) { return 32 * (dim == 64 ? kPromptWaves<64> : dim == 128 ? kPromptWaves<128> : kPromptWaves<256>); }
+
+int kv8_prompt_resident(int dim) {
+  return dim == 64 ? 4 * kPromptOccupancy<64> / kPromptWaves<64>
+                   : dim == 128 ? 4 * kPromptOccupancy<128> / kPromptWaves<128> : 4 * kPromptOccupancy<256> / kPromptWaves<256>;
+}
 
 size_t kv8_prompt_partial(int dim) { return static_cast<size_t>(kv8_prompt_rows(dim)) * 2 * (dim / 2 + 2) * sizeof(float); }
 
