@@ -404,11 +404,12 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   if (nt) {
     splits = (tiles + std::max<long long>(a->waves, share) - 1) / std::max<long long>(a->waves, share);
   } else {
-    // rounds of the workgroups over the compute units, times a workgroup's tiles and
-    // what its beginning and end (and joining splits) cost in tiles
+    // Fewer workgroups than run at once: the rounds of the splits over the compute
+    // units, times a split's tiles and what its beginning and end (and the joining)
+    // cost in tiles.
     const long long slots = static_cast<long long>(cus) * kv8_prompt_resident(a->c.dim);
     long long best = -1;
-    for (long long n = 1; n <= kMostSplits && n <= std::max<long long>(tiles / 2, 1); ++n) {
+    for (long long n = 1; units < slots && n <= kMostSplits && n <= std::max<long long>(tiles / 2, 1); ++n) {
       const long long cost = ((units * n + slots - 1) / slots) * ((tiles + n - 1) / n + (n > 1 ? 6 : 3));
       if (best < 0 || cost < best) best = cost, splits = n;
     }

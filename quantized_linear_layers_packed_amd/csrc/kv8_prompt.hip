@@ -26,12 +26,13 @@ namespace qlin {
 namespace {
 
 // Waves of a workgroup, and of a SIMD.  A code is converted once per workgroup, so
-// more waves convert less; heads of 256 dimensions fill the registers with one
-// wave per SIMD, those of 64 leave room for three.
+// more waves convert less (prompt of 8192 with heads of 128: 8 waves 1.24, 4 waves
+// 1.31 ms); heads of 256 dimensions fill the registers with one wave per SIMD.  A
+// third wave for heads of 64 changes nothing.
 template <int D>
 constexpr int kPromptWaves = D == 128 ? 8 : 4;
 template <int D>
-constexpr int kPromptOccupancy = D > 128 ? 1 : D > 64 ? 2 : 3;
+constexpr int kPromptOccupancy = D > 128 ? 1 : 2;
 
 // A run of 16 tokens of a tile: its key scale, log2 and reciprocal of its value
 // scale.
@@ -205,8 +206,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
             st[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.k[32 * T + krow][16 * s + 8 * h]), qf[s],
                                                            st[T], 0, 0, 0);
         }
-        if constexpr (D > 64) lookahead<2 * KS>();            // (narrow heads have no registers for it)
-        else __builtin_amdgcn_sched_barrier(0);
+        lookahead<2 * KS>();
         float c[4], lv[4], iv[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const h8_t*>(&now.v[32 * d + ql][16 * s + 8 * h]), pf[s],
                                                           o[d], 0, 0, 0);
         put_codes(tile[(x - x0 + 1) & 1]);
-        if constexpr (D > 64) lookahead<4 * DT>();
+        lookahead<4 * DT>();
       }
     }
     l = sum_over_32(l);
