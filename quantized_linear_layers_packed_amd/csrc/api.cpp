@@ -500,6 +500,7 @@ qlin_status qlin_kv8_append(const qlin_kv8_cache* cache, const qlin_kv8_batch* b
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.q_heads = q_heads;
+  a.group = Q ? q_heads / a.c.heads : 0;
   a.cos = cos;
   a.sin = sin;
   a.max_pos = max_pos;

@@ -48,7 +48,7 @@ struct Kv8AppendArgs {
   const uint16_t* K;
   const uint16_t* V;
   long long q_stride, k_stride, v_stride;
-  int q_heads;
+  int q_heads, group;   // group: query heads that share a key/value head
   const float* cos;
   const float* sin;
   int max_pos, rot, pairs;

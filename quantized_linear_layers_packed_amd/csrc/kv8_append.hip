@@ -66,29 +66,36 @@ __device__ __forceinline__ void item_chunks(int p, int rot, int pairs, int* c0, 
   *c1 = halves ? p + rot / 16 : 2 * p + 1;
 }
 
-// x[0..7], x[8..15]: the item's two chunks, turned in place.
-__device__ __forceinline__ void rotate_item(float* x, int p, int pos, const Kv8AppendArgs& a) {
-  if (16 * p >= a.rot) return;
-  const size_t at = static_cast<size_t>(min(pos, a.max_pos - 1)) * (a.rot / 2) + 8 * p;
+// Cosines and sines of an item that turns, at a position.
+struct Turn {
   float c[8], s[8];
+};
+__device__ __forceinline__ Turn load_turn(int p, int pos, const Kv8AppendArgs& a) {
+  Turn t;
+  const size_t at = static_cast<size_t>(min(pos, a.max_pos - 1)) * (a.rot / 2) + 8 * p;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    *reinterpret_cast<float4*>(c + 4 * j) = reinterpret_cast<const float4*>(a.cos + at)[j];
-    *reinterpret_cast<float4*>(s + 4 * j) = reinterpret_cast<const float4*>(a.sin + at)[j];
+    *reinterpret_cast<float4*>(t.c + 4 * j) = reinterpret_cast<const float4*>(a.cos + at)[j];
+    *reinterpret_cast<float4*>(t.s + 4 * j) = reinterpret_cast<const float4*>(a.sin + at)[j];
   }
-  if (a.pairs) {
+  return t;
+}
+
+// x[0..7], x[8..15]: the item's two chunks, turned in place.
+__device__ __forceinline__ void turn_item(float* x, const Turn& t, int pairs) {
+  if (pairs) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float u = x[2 * j], v = x[2 * j + 1];
-      x[2 * j] = u * c[j] - v * s[j];
-      x[2 * j + 1] = v * c[j] + u * s[j];
+      x[2 * j] = u * t.c[j] - v * t.s[j];
+      x[2 * j + 1] = v * t.c[j] + u * t.s[j];
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float u = x[j], v = x[8 + j];
-      x[j] = u * c[j] - v * s[j];
-      x[8 + j] = v * c[j] + u * s[j];
+      x[j] = u * t.c[j] - v * t.s[j];
+      x[8 + j] = v * t.c[j] + u * t.s[j];
     }
   }
 }
@@ -137,7 +144,7 @@ template <bool BF16, int NP>
 __device__ __forceinline__ void store_page(const Kv8AppendArgs& a, const Kv8Seq& q, int head, int page, int lo, int hi,
                                            uint8_t* turn, uint32_t (*red)[8]) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int D = a.c.dim, P = 1 << a.c.log_page, DP = D / 16;
+  const int D = a.c.dim, P = 1 << a.c.log_page, log_dp = __ffs(D) - 5, DP = 1 << log_dp;   // DP work items a token
   const int base = lo & ~(P - 1), olds = lo - base, fresh = hi - lo;
   const size_t at = (static_cast<size_t>(page) * a.c.heads + head) * P * D;
   int8_t* kp = a.c.k + at;
@@ -149,7 +156,7 @@ __device__ __forceinline__ void store_page(const Kv8AppendArgs& a, const Kv8Seq&
   uint32_t mk = 0, mv = 0;
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
-    const int i = tid + n * nt, t = i / DP, p = i - t * DP;
+    const int i = tid + n * nt, t = i >> log_dp, p = i & (DP - 1);
     if (t < fresh) {
       const size_t row = static_cast<size_t>(q.row + (lo - q.start) + t);
       int c0, c1;
@@ -160,7 +167,7 @@ __device__ __forceinline__ void store_page(const Kv8AppendArgs& a, const Kv8Seq&
       widen8<BF16>(kr[c1], kx[n] + 8);
       widen8<BF16>(vr[2 * p], vx[n]);
       widen8<BF16>(vr[2 * p + 1], vx[n] + 8);
-      rotate_item(kx[n], p, lo + t, a);
+      if (16 * p < a.rot) turn_item(kx[n], load_turn(p, lo + t, a), a.pairs);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         mk = max(mk, bitcast<uint32_t>(kx[n][j]) & 0x7FFFFFFFu);
@@ -188,7 +195,7 @@ __device__ __forceinline__ void store_page(const Kv8AppendArgs& a, const Kv8Seq&
   // keys, and the values' codes into the transposed page in LDS
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
-    const int i = tid + n * nt, t = i / DP, p = i - t * DP;
+    const int i = tid + n * nt, t = i >> log_dp, p = i & (DP - 1);
     if (t < fresh) {
       int c0, c1;
       item_chunks(p, a.rot, a.pairs, &c0, &c1);
@@ -250,25 +257,50 @@ __global__ __launch_bounds__(512) void kv8_append_kernel(const Kv8AppendArgs a) 
     }
     return;
   }
-  // queries: P tokens at a time, the head's whole group
-  const int D = a.c.dim, DP = D / 16, G = a.q_heads / a.c.heads;
+  // queries: P tokens at a time; an item's cosines and sines serve the heads of the
+  // group, which are dealt out over the threads that few tokens leave idle
+  const int D = a.c.dim, log_dp = __ffs(D) - 5, G = a.group;
+  const size_t stride = static_cast<size_t>(D) / 8;         // between heads, in chunks
   for (long long t0 = static_cast<long long>(blockIdx.x) << a.c.log_page; t0 < q.count;
        t0 += static_cast<long long>(gridDim.x) << a.c.log_page) {
-    const int n = min(P, q.count - static_cast<int>(t0)) * G * DP;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int r = i / DP, p = i - r * DP;
-      const int t = r / G, h = head * G + (r - t * G);
+    const int n = min(P, q.count - static_cast<int>(t0)) << log_dp;
+    const int deals = min(max(static_cast<int>(blockDim.x) / n, 1), G);
+    for (int k = threadIdx.x; k < n * deals; k += blockDim.x) {
+      const int deal = deals > 1 ? k / n : 0, i = k - deal * n;
+      const int t = i >> log_dp, p = i & ((1 << log_dp) - 1);
       const size_t row = static_cast<size_t>(q.row + t0 + t);
       int c0, c1;
       item_chunks(p, a.rot, a.pairs, &c0, &c1);
-      const uint4* src = reinterpret_cast<const uint4*>(a.Q + row * a.q_stride + static_cast<size_t>(h) * D);
-      uint4* dst = reinterpret_cast<uint4*>(a.Q_out + (row * a.q_heads + h) * D);
-      float x[16];
-      widen8<BF16>(src[c0], x);
-      widen8<BF16>(src[c1], x + 8);
-      rotate_item(x, p, max(q.start + static_cast<int>(t0) + t, 0), a);
-      dst[c0] = narrow8<BF16>(x);
-      dst[c1] = narrow8<BF16>(x + 8);
+      const uint4* src = reinterpret_cast<const uint4*>(a.Q + row * a.q_stride + static_cast<size_t>(head) * G * D);
+      uint4* dst = reinterpret_cast<uint4*>(a.Q_out + (row * a.q_heads + static_cast<size_t>(head) * G) * D);
+      const bool turns = 16 * p < a.rot;
+      Turn turn;
+      if (turns) turn = load_turn(p, max(q.start + static_cast<int>(t0) + t, 0), a);
+      constexpr int AHEAD = 4;                              // heads on their way
+      for (int h0 = deal; h0 < G; h0 += AHEAD * deals) {
+        uint4 w[AHEAD][2];
+#pragma unroll
+        for (int h = 0; h < AHEAD; ++h) {
+          const uint4* s = src + min(h0 + h * deals, G - 1) * stride;
+          w[h][0] = s[c0];
+          w[h][1] = s[c1];
+        }
+#pragma unroll
+        for (int h = 0; h < AHEAD; ++h) {
+          if (h0 + h * deals >= G) break;
+          if (turns) {
+            float x[16];
+            widen8<BF16>(w[h][0], x);
+            widen8<BF16>(w[h][1], x + 8);
+            turn_item(x, turn, a.pairs);
+            w[h][0] = narrow8<BF16>(x);
+            w[h][1] = narrow8<BF16>(x + 8);
+          }
+          uint4* d = dst + (h0 + h * deals) * stride;
+          d[c0] = w[h][0];
+          d[c1] = w[h][1];
+        }
+      }
     }
   }
 }
@@ -279,14 +311,14 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void kv8_gather_kernel(const Kv8View c, uint16_t* __restrict__ K,
                                                          uint16_t* __restrict__ V) {
   extern __shared__ __align__(16) uint8_t turn[];
-  const int tid = threadIdx.x, D = c.dim, P = 1 << c.log_page, DP = D / 16, head = blockIdx.y;
+  const int tid = threadIdx.x, D = c.dim, P = 1 << c.log_page, log_dp = __ffs(D) - 5, DP = 1 << log_dp, head = blockIdx.y;
   const int stride = P + 4;                                // bytes per dimension: neighbours in other banks
   const Kv8Seq q = kv8_seq(c, blockIdx.z);
   if (q.count == 0) return;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   if (blockIdx.x == 0) {                                   // positions below 0: nothing stored
     for (int i = tid; i < min(q.count, max(-q.start, 0)) * DP; i += blockDim.x) {
-      const int t = i / DP, p = i - t * DP;
+      const int t = i >> log_dp, p = i & (DP - 1);
       const size_t o = ((static_cast<size_t>(q.row + t) * c.heads + head) * D + 16 * p) / 8;
       reinterpret_cast<uint4*>(K)[o] = reinterpret_cast<uint4*>(K)[o + 1] = zero;
       reinterpret_cast<uint4*>(V)[o] = reinterpret_cast<uint4*>(V)[o + 1] = zero;
@@ -309,7 +341,7 @@ __global__ __launch_bounds__(256) void kv8_gather_kernel(const Kv8View c, uint16
     }
     __syncthreads();
     for (int i = tid; i < (hi - lo) * DP; i += blockDim.x) {
-      const int t = i / DP, p = i - t * DP;
+      const int t = i >> log_dp, p = i & (DP - 1);
       const size_t row = static_cast<size_t>(q.row + (lo - q.start) + t);
       const uint4 w = *reinterpret_cast<const uint4*>(kp + static_cast<size_t>(s0 + t) * D + 16 * p);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
