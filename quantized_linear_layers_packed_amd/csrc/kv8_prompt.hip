@@ -19,7 +19,6 @@
 #include "device.hpp"
 #include "kv8.hpp"
 #include "kv8_device.hpp"
-#include "splitk.hpp"
 
 namespace qlin {
 
@@ -66,14 +65,35 @@ __device__ __forceinline__ void lookahead() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// A row tile: rows r0 .. r0 + nrows - 1 of a sequence, the tiles they see and how
+// many of them a split takes.  Row tiles beyond those planned for are not split:
+// their partial results would share workspace with the first ones'.
+template <int D>
+struct RowTile {
+  static constexpr int ROWS = 32 * kPromptWaves<D>;
+  int nrows, p0, p1;
+  Kv8Tiles tiles;
+  int per, used;
+  __device__ __forceinline__ RowTile(const Kv8AttnArgs& a, const Kv8Seq& seq, int rows, int r0)
+      : nrows(min(rows - r0, ROWS)), p0(seq.start + a.by_group(r0)), p1(seq.start + a.by_group(r0 + nrows - 1)),
+        tiles(p0, p1, a.window, a.sinks) {
+    const bool planned = r0 < a.row_tiles * ROWS;
+    per = planned ? max(a.chunk, a.by_splits(tiles.count + a.splits - 1)) : max(tiles.count, 1);
+    used = per >= tiles.count ? 1 : (tiles.count + per - 1) / per;
+  }
+};
+
+// Floats of a split's partial result: per wave and lane its 16 DT sums, the
+// reference and the sum of weights.
+template <int D>
+constexpr int kPromptSlot = kPromptWaves<D> * 64 * (D / 2 + 2);
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8_prompt_kernel(const Kv8AttnArgs a) {
   constexpr int W = kPromptWaves<D>, NT = 64 * W, ROWS = 32 * W, DT = D / 32, KS = D / 16;
   constexpr int NL = D * kTile / 16 / NT;                  // 16-byte pieces of K (and of V) per thread and tile
-  constexpr int SLOT = W * 64 * (16 * DT + 2);             // floats of a split's partial result
   extern __shared__ __align__(16) char smem[];
   Tile16<D>* tile = reinterpret_cast<Tile16<D>*>(smem);    // two of them
-  __shared__ int flag;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, h = lane >> 5, ql = lane & 31;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
   const int b = a.by_row_tiles(unit), split = blockIdx.y;
@@ -86,16 +106,11 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
   // Row tiles from the last, which sees the most, to the first; row tiles past
   // the grid are taken up in turn.
   for (int r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * ROWS; r0 < rows; r0 += a.row_tiles * ROWS) {
-    const int nrows = min(rows - r0, ROWS);
-    const int p0 = seq.start + a.by_group(r0), p1 = seq.start + a.by_group(r0 + nrows - 1);
-    const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
-    // row tiles beyond those planned for are not split: their partial results
-    // would share workspace with the first ones'
-    const bool planned = r0 < a.row_tiles * ROWS;
-    const int per = planned ? max(a.chunk, a.by_splits(tiles.count + a.splits - 1)) : max(tiles.count, 1);
-    if (split > 0 && split * per >= tiles.count) continue;
-    const int used = per >= tiles.count ? 1 : (tiles.count + per - 1) / per;
-    const int x0 = split * per, x1 = min(x0 + per, tiles.count);
+    const RowTile<D> rt(a, seq, rows, r0);
+    const int nrows = rt.nrows, p0 = rt.p0, p1 = rt.p1;
+    const Kv8Tiles& tiles = rt.tiles;
+    if (split >= rt.used) continue;
+    const int x0 = split * rt.per, x1 = min(x0 + rt.per, tiles.count);
 
     // this lane's row
     const int r = r0 + min(32 * wv + ql, nrows - 1), t = a.by_group(r), hq = head * G + r - t * G;
@@ -287,40 +302,18 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     }
     l = sum_over_32(l);
 
-    if (used > 1) {
-      // every value of the partial result at its register's and lane's own place
+    if (rt.used > 1) {
+      // every value at its register's and lane's own place, for the joining kernel
       int place = wv * 64 * (16 * DT + 2) + lane;
       asm volatile("" : "+v"(place));                       // its 16 DT addresses are not to be held through the loop
-      float* slots = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * SLOT + place;
-      float* part = slots + static_cast<size_t>(split) * SLOT;
+      float* part = a.partials + (static_cast<size_t>(blockIdx.x) * a.splits + split) * kPromptSlot<D> + place;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sk_store(part + 64 * (16 * d + i), o[d][i]);
-      sk_store(part + 64 * 16 * DT, m);
-      sk_store(part + 64 * 16 * DT + 64, l);
-      if (!sk_arrive_last(a.counters + blockIdx.x, used - 1, &flag)) continue;
-      m = kNone;
-      for (int k = 0; k < used; ++k) m = fmaxf(m, sk_load(slots + static_cast<size_t>(k) * SLOT + 64 * 16 * DT));
-      l = 0.0f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-      for (int k = 0; k < used; ++k) {
-        const float* q = slots + static_cast<size_t>(k) * SLOT;
-        const float f = __builtin_amdgcn_exp2f(sk_load(q + 64 * 16 * DT) - m);
-        l = fmaf(sk_load(q + 64 * 16 * DT + 64), f, l);
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][i] = fmaf(sk_load(q + 64 * (16 * d + i)), f, o[d][i]);
-          __builtin_amdgcn_sched_barrier(0);                // at most 16 loads' registers
-        }
-      }
-      if (tid == 0) sk_reset(a.counters + blockIdx.x);
-    }
-    if (mine) {
+        for (int i = 0; i < 16; ++i) part[64 * (16 * d + i)] = o[d][i];
+      part[64 * 16 * DT] = m;
+      part[64 * 16 * DT + 64] = l;
+    } else if (mine) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       int again = tid;
       asm volatile("" : "+v"(again));                       // (nothing of the address to be held through the loop)
@@ -332,8 +325,59 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
           *reinterpret_cast<uint2*>(y + 32 * d + 2 * i) =
               make_uint2(pack2<BF16>(o[d][i] * inv, o[d][i + 1] * inv), pack2<BF16>(o[d][i + 2] * inv, o[d][i + 3] * inv));
     }
-    __syncthreads();                                        // tiles and flag may be used for the next rows
+    __syncthreads();                                        // the tiles may be used for the next rows
   }
+}
+
+// Joins the splits of row tiles, in their order: a wave per row tile, wave of it
+// and group of four sums, spread over the whole device (one workgroup joining 64
+// splits of 256 rows would read 9 MB by itself).
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void kv8_prompt_join_kernel(const Kv8AttnArgs a) {
+  constexpr int W = kPromptWaves<D>, GROUPS = D / 8, AHEAD = 8;
+  const int lane = threadIdx.x & 63, h = lane >> 5, ql = lane & 31;
+  const int task = blockIdx.y * 4 + (threadIdx.x >> 6), wv = task / GROUPS, group = task % GROUPS;
+  const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads, b = a.by_row_tiles(unit);
+  const Kv8Seq seq = kv8_seq(a.c, b);
+  const int rows = seq.count * a.group, r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * RowTile<D>::ROWS;
+  if (r0 >= rows) return;
+  const RowTile<D> rt(a, seq, rows, r0);
+  if (rt.used == 1) return;
+  const float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * kPromptSlot<D> + wv * 64 * (D / 2 + 2) + lane;
+  const float* stats = part + 64 * (D / 2);
+  float m = kNone;
+  for (int k = 0; k < rt.used; k += AHEAD) {
+    float v[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) v[j] = stats[static_cast<size_t>(min(k + j, rt.used - 1)) * kPromptSlot<D>];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) m = fmaxf(m, v[j]);
+  }
+  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < rt.used; k += AHEAD) {
+    float ref[AHEAD], sum[AHEAD], v[AHEAD][4];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const size_t at = static_cast<size_t>(min(k + j, rt.used - 1)) * kPromptSlot<D>;
+      ref[j] = stats[at];
+      sum[j] = stats[at + 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = part[at + 64 * (4 * group + i)];
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (k + j >= rt.used) break;
+      const float f = __builtin_amdgcn_exp2f(ref[j] - m);
+      l = fmaf(sum[j], f, l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[j][i], f, o[i]);
+    }
+  }
+  if (32 * wv + ql >= rt.nrows) return;
+  const int r = r0 + 32 * wv + ql, t = a.by_group(r), hq = head * a.group + r - t * a.group;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + 32 * (group >> 2) + 8 * (group & 3) + 4 * h;
+  *reinterpret_cast<uint2*>(y) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
 }
 
 template <int D>
@@ -342,6 +386,11 @@ void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   const size_t lds = 2 * sizeof(Tile16<D>);
   const auto fn = dtype == QLIN_BF16 ? kv8_prompt_kernel<D, true> : kv8_prompt_kernel<D, false>;
   hipLaunchKernelGGL(fn, grid, block, lds, stream, a);
+  if (a.splits > 1) {
+    const dim3 tasks(grid.x, kPromptWaves<D> * (D / 8) / 4);
+    const auto join = dtype == QLIN_BF16 ? kv8_prompt_join_kernel<D, true> : kv8_prompt_join_kernel<D, false>;
+    hipLaunchKernelGGL(join, tasks, dim3(256), 0, stream, a);
+  }
 }
 
 }  // namespace
@@ -353,7 +402,9 @@ int kv8_prompt_resident(int dim) {
                    : dim == 128 ? 4 * kPromptOccupancy<128> / kPromptWaves<128> : 4 * kPromptOccupancy<256> / kPromptWaves<256>;
 }
 
-size_t kv8_prompt_partial(int dim) { return static_cast<size_t>(kv8_prompt_rows(dim)) * 2 * (dim / 2 + 2) * sizeof(float); }
+size_t kv8_prompt_partial(int dim) {
+  return sizeof(float) * (dim == 64 ? kPromptSlot<64> : dim == 128 ? kPromptSlot<128> : kPromptSlot<256>);
+}
 
 void kv8_prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   switch (a.c.dim) {
