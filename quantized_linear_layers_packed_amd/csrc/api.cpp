@@ -237,7 +237,7 @@ int64_t kv8_span(int tokens, int heads, int dim, int64_t stride) {
 }
 
 qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, int q_heads,
-                          int window, int sinks, bool sizes_only, Kv8AttnArgs* a, size_t* total) {
+                          int window, int sinks, bool sizes_only, Kv8AttnArgs* a, Kv8AttnPlan* plan, size_t* total) {
   QLIN_TRY(kv8_view(fn, cache, batch, sizes_only, &a->c));
   QLIN_TRY(kv8_check_heads(fn, q_heads, a->c.heads));
   if (window < 0 || sinks < 0) return fail(QLIN_EINVAL, std::string(fn) + ": window and sinks must not be negative");
@@ -248,8 +248,9 @@ qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qli
   a->group = q_heads / a->c.heads;
   a->window = window;
   a->sinks = sinks;
-  const size_t partial = kv8_attn_plan(a);
-  *total = partial ? kCounterBytes + ws_round(partial) : 0;
+  *plan = kv8_attn_plan(*a);
+  const size_t partial = plan->few_bytes + plan->many_bytes;
+  *total = partial ? kCounterBytes + partial : 0;
   return QLIN_OK;
 }
 
@@ -531,7 +532,8 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
   clear_error();
   if (!bytes) return fail(QLIN_EINVAL, std::string(fn) + ": NULL bytes");
   Kv8AttnArgs a{};
-  return kv8_attn_args(fn, cache, batch, q_heads, window, sinks, true, &a, bytes);
+  Kv8AttnPlan plan;
+  return kv8_attn_args(fn, cache, batch, q_heads, window, sinks, true, &a, &plan, bytes);
 }
 
 qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, const void* Q, int dtype,
@@ -540,8 +542,14 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
   static const char* fn = "qlin_kv8_attention";
   clear_error();
   Kv8AttnArgs a{};
+  // (the plan copies these)
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.q_stride = q_stride;
+  a.scale = scale * 1.44269504088896340736f;   // log2(e)
+  a.Y = static_cast<uint16_t*>(Y);
+  Kv8AttnPlan plan;
   size_t total = 0;
-  QLIN_TRY(kv8_attn_args(fn, cache, batch, q_heads, window, sinks, false, &a, &total));
+  QLIN_TRY(kv8_attn_args(fn, cache, batch, q_heads, window, sinks, false, &a, &plan, &total));
   QLIN_TRY(kv8_check_dtype(fn, dtype));
   if (!Q || !Y) return fail(QLIN_EINVAL, std::string(fn) + ": NULL Q or Y");
   if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QLIN_EINVAL, std::string(fn) + ": scale must be finite and positive");
@@ -552,16 +560,8 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
                   kv8_span(a.c.tokens, q_heads, a.c.dim, static_cast<int64_t>(q_heads) * a.c.dim)))
     return fail(QLIN_EINVAL, std::string(fn) + ": Y overlaps Q");
   QLIN_TRY(need_workspace(fn, workspace, workspace_bytes, total));
-  a.Q = static_cast<const uint16_t*>(Q);
-  a.q_stride = q_stride;
-  a.scale = scale * 1.44269504088896340736f;   // log2(e)
-  a.Y = static_cast<uint16_t*>(Y);
-  if (total) {
-    const WsView ws{static_cast<char*>(workspace), workspace_bytes};
-    a.counters = ws.counters();
-    a.partials = static_cast<float*>(ws.partials());
-  }
-  kv8_attn_launch(a, dtype, stream);
+  const WsView ws{static_cast<char*>(workspace), workspace_bytes};
+  kv8_attn_launch(plan, total ? ws.counters() : nullptr, total ? static_cast<char*>(ws.partials()) : nullptr, dtype, stream);
   return check_launch(fn);
 }
 

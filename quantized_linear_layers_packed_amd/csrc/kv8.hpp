@@ -79,8 +79,9 @@ struct Kv8AttnArgs {
   float scale;          // times log2(e)
   int window, sinks;    // window 0: none (sinks then 0)
   uint16_t* Y;
+  int least_rows, most_rows;   // of a sequence that this launch computes
   // the split of long sequences (see kv8_attn.hip)
-  int row_tiles, splits, chunk, waves;
+  int row_columns, row_tiles, splits, chunk, waves;
   bool sorted;          // sequences in the order of their lengths
   FastDiv by_group, by_heads, by_row_tiles, by_splits;
   int* counters;
@@ -90,10 +91,16 @@ struct Kv8AttnArgs {
 void kv8_append_launch(const Kv8AppendArgs& a, int dtype, hipStream_t stream);
 void kv8_gather_launch(const Kv8View& c, uint16_t* K, uint16_t* V, int dtype, hipStream_t stream);
 
-// Fills in the split; returns the workspace bytes beyond the counters (0: the
-// call needs no workspace).
-size_t kv8_attn_plan(Kv8AttnArgs* a);
-void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream);
+// The launches of a call, each for the sequences whose number of rows suits it,
+// and the workspace bytes beyond the counters (0: the call needs no workspace).
+struct Kv8AttnPlan {
+  Kv8AttnArgs few, many;
+  bool has_few, has_many;
+  size_t few_bytes, many_bytes;
+};
+Kv8AttnPlan kv8_attn_plan(const Kv8AttnArgs& a);
+// With the workspace's counters and the memory after them.
+void kv8_attn_launch(Kv8AttnPlan p, int* counters, char* partials, int dtype, hipStream_t stream);
 // The kernel for many rows: rows of a workgroup, workgroups that share a compute
 // unit, bytes of a split's partial result.
 int kv8_prompt_rows(int dim);

@@ -102,6 +102,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int P = 1 << a.c.log_page, G = a.group;
   const int rows = seq.count * G;                             // below 2^30
+  if (rows < a.least_rows || rows > a.most_rows) return;
   // row tiles past the grid are taken up in turn
   for (int r0 = (unit - rank * a.row_tiles) * (16 * NT); r0 < rows; r0 += a.row_tiles * (16 * NT)) {
     const int nrows = min(rows - r0, 16 * NT);
@@ -359,10 +360,20 @@ void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
 }
 
 // 16-row column tiles per wave of the kernel for few rows, 0 for the kernel for
-// many rows.  Heads of 256 dimensions have registers for one.
-int rows_nt(const Kv8AttnArgs& a) {
-  const long long rows = static_cast<long long>(a.c.max_new) * a.group;
-  return rows <= 16 ? 1 : rows <= 32 && a.c.dim <= 128 ? 2 : 0;
+// many rows.  Up to 128 rows one column tile with a workgroup for each 16 rows is
+// fastest while these are too few to fill the device, although each reads the
+// cache (64 rows over 32768 tokens of 4 heads: 27 us, with two column tiles 36, the
+// kernel for many rows 51); then two column tiles (64 sequences of 2048 tokens, 64
+// rows each: 66, 55 and 81 us; 128 rows each: 116, 93 and 85 us).  Heads of 256
+// dimensions have registers for one column tile.
+int rows_nt(const Kv8AttnArgs& a, int cus) {
+  const long long rows = static_cast<long long>(a.c.max_new) * a.group, per_tile = static_cast<long long>(a.c.seqs) * a.c.heads;
+  const long long units = per_tile * ((rows + 15) / 16);
+  if (rows <= 16) return 1;
+  if (a.c.dim > 128) return rows <= 64 && units <= 2LL * cus ? 1 : 0;
+  if (rows <= 64) return units <= (rows <= 32 ? cus / 4 : cus) ? 1 : 2;
+  if (rows <= 128) return units <= cus / 2 ? 1 : per_tile * ((rows + 31) / 32) <= cus ? 2 : 0;
+  return 0;
 }
 
 // Waves of a workgroup.  With 4, two workgroups share a compute unit and one's
@@ -378,11 +389,11 @@ int rows_waves(const Kv8AttnArgs& a, int nt, long long units, long long tiles, i
   return nt == 2 || (tiles >= 64 && units * tiles >= 64LL * cus && units <= 2LL * cus) ? 8 : 4;
 }
 
-}  // namespace
-
-size_t kv8_attn_plan(Kv8AttnArgs* a) {
-  const int nt = rows_nt(*a), cus = device_cus();
-  const long long rows = static_cast<long long>(a->c.max_new) * a->group, tile_rows = nt ? 16 * nt : kv8_prompt_rows(a->c.dim);
+// The launch of one kernel for sequences of up to `rows` rows (nt as above): its
+// grid and splits; returns the bytes of its partial results.
+size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
+  a->row_columns = nt;
+  const long long tile_rows = nt ? 16 * nt : kv8_prompt_rows(a->c.dim);
   const long long most = std::min(std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads)), 65535LL);
   a->row_tiles = static_cast<int>(std::min((rows + tile_rows - 1) / tile_rows, most));
   long long tiles = (static_cast<long long>(a->c.max_kv) + kTile - 1) / kTile;
@@ -399,22 +410,20 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   a->by_splits = FastDiv(1);
   a->chunk = static_cast<int>(tiles);
   if (units > kCounterSlots) return 0;
-  const long long share = (units * tiles + cus - 1) / cus;    // tiles per compute unit
-  long long splits = 1;
-  if (nt) {
-    splits = (tiles + std::max<long long>(a->waves, share) - 1) / std::max<long long>(a->waves, share);
-  } else {
-    // Fewer workgroups than run at once: the rounds of the splits over the compute
-    // units, times a split's tiles and what its beginning and end (and the joining)
-    // cost in tiles.
-    const long long slots = static_cast<long long>(cus) * kv8_prompt_resident(a->c.dim);
-    long long best = -1;
-    for (long long n = 1; units < slots && n <= kMostSplits && n <= std::max<long long>(tiles / 2, 1); ++n) {
-      const long long cost = ((units * n + slots - 1) / slots) * ((tiles + n - 1) / n + (n > 1 ? 6 : 3));
-      if (best < 0 || cost < best) best = cost, splits = n;
-    }
+  // Splits: the rounds of the workgroups over the device, times a workgroup's steps
+  // (of W tiles; the kernel for many rows takes one at a time) and what its
+  // beginning and end, and joining splits, cost in steps.  One workgroup to a
+  // compute unit, also where two would fit: twice the splits cost more than they
+  // hide (131072 tokens 50 -> 59 us).  Row tiles of a prompt differ in length and
+  // are not split once there is one for every workgroup that fits.
+  const long long slots = static_cast<long long>(cus) * (nt ? 1 : kv8_prompt_resident(a->c.dim));
+  const long long steps = nt ? a->waves : 1, alone = 3, split = nt ? 5 : 6;
+  long long splits = 1, best = -1;
+  for (long long n = 1; (nt || units < slots) && n <= kMostSplits && n <= std::max<long long>(tiles / 2, 1); ++n) {
+    const long long each = ((tiles + n - 1) / n + steps - 1) / steps;
+    const long long cost = ((units * n + slots - 1) / slots) * (each + (n > 1 ? split : alone));
+    if (best < 0 || cost < best) best = cost, splits = n;
   }
-  splits = std::min<long long>(splits, kMostSplits);
   a->splits = static_cast<int>(splits);
   a->by_splits = FastDiv(a->splits);
   a->chunk = static_cast<int>((tiles + splits - 1) / splits);
@@ -423,12 +432,8 @@ size_t kv8_attn_plan(Kv8AttnArgs* a) {
   return static_cast<size_t>(units) * splits * partial;
 }
 
-void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
-  const int nt = rows_nt(a);
-  if (nt == 0) {
-    kv8_prompt_launch(a, dtype, stream);
-    return;
-  }
+void few_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
+  const int nt = a.row_columns;
   const bool wide = a.waves == 8;
   switch (a.c.dim) {
     case 64:
@@ -440,6 +445,46 @@ void kv8_attn_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
       else wide ? rows_launch<128, 1, 8>(a, dtype, stream) : rows_launch<128, 1, 4>(a, dtype, stream);
       break;
     default: rows_launch<256, 1, 4>(a, dtype, stream); break;
+  }
+}
+
+constexpr int kFewRows = 16;              // one column tile
+constexpr int kMixedSeqs = 8;
+
+}  // namespace
+
+// Where the longest sequence wants the kernel for many rows, batches of eight and
+// more sequences may well hold single tokens too (prompts that join a running
+// batch): those then have a launch of the kernel for few rows of their own, which
+// costs 3 us when there are none.
+Kv8AttnPlan kv8_attn_plan(const Kv8AttnArgs& a) {
+  Kv8AttnPlan p{};
+  const int cus = device_cus();
+  const long long rows = static_cast<long long>(a.c.max_new) * a.group;
+  p.few = p.many = a;
+  p.few.least_rows = p.many.least_rows = 0;
+  p.few.most_rows = p.many.most_rows = INT32_MAX;
+  const int nt = rows_nt(a, cus);
+  p.has_many = nt == 0;
+  p.has_few = nt != 0 || a.c.seqs >= kMixedSeqs;
+  if (p.has_few) p.few_bytes = ws_round(plan_launch(&p.few, nt ? nt : 1, nt ? rows : kFewRows, cus));
+  if (p.has_many) p.many_bytes = ws_round(plan_launch(&p.many, 0, rows, cus));
+  if (p.has_few && p.has_many) {
+    p.few.most_rows = kFewRows;
+    p.many.least_rows = kFewRows + 1;
+  }
+  return p;
+}
+
+void kv8_attn_launch(Kv8AttnPlan p, int* counters, char* partials, int dtype, hipStream_t stream) {
+  if (p.has_many) {
+    p.many.partials = reinterpret_cast<float*>(partials + p.few_bytes);
+    kv8_prompt_launch(p.many, dtype, stream);
+  }
+  if (p.has_few) {
+    p.few.counters = counters;
+    p.few.partials = reinterpret_cast<float*>(partials);
+    few_launch(p.few, dtype, stream);
   }
 }
 

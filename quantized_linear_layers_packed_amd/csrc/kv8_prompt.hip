@@ -100,6 +100,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int P = 1 << a.c.log_page, G = a.group;
   const int rows = seq.count * G;                             // below 2^30
+  if (rows < a.least_rows || rows > a.most_rows) return;
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
   const int last_entry = (seq.len - 1) >> a.c.log_page;    // entries past it are not read
 
@@ -334,13 +335,13 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
 // splits of 256 rows would read 9 MB by itself).
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void kv8_prompt_join_kernel(const Kv8AttnArgs a) {
-  constexpr int W = kPromptWaves<D>, GROUPS = D / 8, AHEAD = 8;
+  constexpr int GROUPS = D / 8, AHEAD = 8;
   const int lane = threadIdx.x & 63, h = lane >> 5, ql = lane & 31;
   const int task = blockIdx.y * 4 + (threadIdx.x >> 6), wv = task / GROUPS, group = task % GROUPS;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads, b = a.by_row_tiles(unit);
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int rows = seq.count * a.group, r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * RowTile<D>::ROWS;
-  if (r0 >= rows) return;
+  if (r0 >= rows || rows < a.least_rows || rows > a.most_rows) return;
   const RowTile<D> rt(a, seq, rows, r0);
   if (rt.used == 1) return;
   const float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * kPromptSlot<D> + wv * 64 * (D / 2 + 2) + lane;

@@ -352,6 +352,22 @@ def test_plans_too_small_or_too_large_still_compute_everything(max_new, max_kv):
     check_round16(q, q_ref, F16)
 
 
+@pytest.mark.parametrize("dtype,D,P,G,window,sinks", [(F16, 64, 16, 4, 0, 0), (BF16, 128, 64, 8, 300, 4), (F16, 256, 32, 3, 0, 0)])
+def test_prompts_among_single_tokens(dtype, D, P, G, window, sinks):
+    """Eight and more sequences of very different lengths in one call: each kernel takes its own, long ones split."""
+    new = [1, 90, 1, 0, 2, 40, 1, 5, 1, 300]
+    kv = [2500, 300, 1, 50, 2, 1900, 63, 5, 700, 300]
+    check_attention(Setup(21, D, P, 1, new, kv), G, dtype, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("D,rows", [(128, 20), (128, 60), (128, 100), (64, 120), (256, 50), (128, 200)])
+def test_every_kernel_choice_by_rows(D, rows):
+    """Row counts around the limits between the kernels, few sequences and many."""
+    for seqs, kv in ((1, 1500), (5, 400), (40, 130)):
+        s = Setup(22, D, 32, 2 if seqs < 40 else 1, [rows // 4] * seqs, [kv + 7 * b for b in range(seqs)])
+        check_attention(s, 4, F16)
+
+
 def test_attention_splits_are_deterministic_and_reuse_their_workspace():
     torch = torch_cuda()
     s = Setup(17, 128, 64, 2, [1, 1], [9000, 4100])
