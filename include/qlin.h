@@ -338,8 +338,8 @@ qlin_status qlin_f16_gemm(const uint16_t* X, const uint16_t* W, int M, int N, in
  *   scales  fp32 [num_pages][kv_heads][2]                    (K scale, V scale)
  *
  * Pages need no initialization: the first append into a page starts its scales.
- * head_dim 64, 128 or 256; page_size 16, 32, 64 or 128 (EUNSUPPORTED otherwise).
- * Offsets into the pool are 64-bit.                                           */
+ * head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; num_pages * kv_heads
+ * below 2^31 (EUNSUPPORTED otherwise).  Offsets into the pool are 64-bit.     */
 typedef struct {
   int8_t* k_codes;
   int8_t* v_codes;
@@ -422,8 +422,14 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  * zeros.
  *   Q device, tokens q_stride elements apart (a multiple of 8), Y device
  *   [tokens][q_heads][head_dim], both of dtype QLIN_F16 or QLIN_BF16; Y must not
- *   overlap Q.  scale: finite, > 0.  tokens * q_heads < 2^30 (EUNSUPPORTED).
+ *   overlap Q.  scale: finite, > 0.  tokens * q_heads < 2^30, seqs * kv_heads
+ *   <= 2^22 (EUNSUPPORTED).
  *   workspace: conventions at the top.
+ * Kernel by the rows max_new * q_heads / kv_heads of a key/value head: up to 128
+ * one that holds 16 or 32 rows and splits the cache over its waves, above that
+ * (from 17 rows on where there are many sequences, from 65 with head_dim 256) one
+ * that holds 128 or 256 rows and shares tiles of the cache; in batches of eight
+ * and more sequences each takes those that suit it.
  * Codes enter the matrix instructions as exact fp16 integers and products are
  * summed in fp32; bf16 queries are scaled to fp16 by a power of two per row (as
  * in qlin_w4_forward); softmax statistics are fp32; the weights are rounded to

@@ -173,6 +173,8 @@ qlin_status kv8_check_sizes(const char* fn, int pages, int heads, int dim, int p
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
     return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": page_size must be 16, 32, 64 or 128");
   if (heads > 32767) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": kv_heads above 32767");
+  if (static_cast<int64_t>(pages) * heads > INT32_MAX)
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": num_pages * kv_heads must be below 2^31");
   return QLIN_OK;
 }
 
@@ -242,6 +244,8 @@ qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qli
   QLIN_TRY(kv8_check_heads(fn, q_heads, a->c.heads));
   if (window < 0 || sinks < 0) return fail(QLIN_EINVAL, std::string(fn) + ": window and sinks must not be negative");
   if (sinks > 0 && window == 0) return fail(QLIN_EINVAL, std::string(fn) + ": sinks without a window");
+  if (static_cast<int64_t>(a->c.seqs) * a->c.heads > (1 << 22))
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": seqs * kv_heads above 2^22");
   if (static_cast<int64_t>(a->c.tokens) * q_heads >= (1 << 30))
     return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": tokens * q_heads must be below 2^30");
   a->q_heads = q_heads;

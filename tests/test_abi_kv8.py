@@ -47,7 +47,7 @@ def test_every_call_checks_cache_and_batch(call):
     for kw, want in (({"num_pages": 0}, EINVAL), ({"kv_heads": -1}, EINVAL), ({"head_dim": 96}, EUNSUPPORTED),
                      ({"page_size": 24}, EUNSUPPORTED), ({"page_size": 0}, EINVAL), ({"k_codes": 0}, EINVAL),
                      ({"v_codes": FAKE + 8}, EALIGN), ({"scales": 0}, EINVAL), ({"scales": FAKE + 4}, EALIGN),
-                     ({"kv_heads": 40000}, EUNSUPPORTED)):
+                     ({"kv_heads": 40000}, EUNSUPPORTED), ({"num_pages": 1 << 30, "kv_heads": 4}, EUNSUPPORTED)):
         assert call(c=cache(**kw)) == want, kw
         assert next(iter(kw)) in qlin.last_error() or "cache" in qlin.last_error()
     for kw, want in (({"seqs": 0}, EINVAL), ({"tokens": 0}, EINVAL), ({"table_stride": 0}, EINVAL), ({"max_new": 0}, EINVAL),
@@ -73,7 +73,7 @@ def test_attention_refusals_and_workspace():
     for kw, want in (({"Q": None}, EINVAL), ({"Y": None}, EINVAL), ({"Y": FAKE + 2}, EALIGN), ({"Q": FAKE + 8}, EALIGN),
                      ({"q_heads": 0}, EINVAL), ({"q_heads": 5}, EINVAL), ({"q_stride": 508}, EINVAL),
                      ({"scale": 0.0}, EINVAL), ({"scale": float("nan")}, EINVAL), ({"scale": float("inf")}, EINVAL),
-                     ({"window": -1}, EINVAL), ({"sinks": -1}, EINVAL), ({"sinks": 4}, EINVAL), ({"Y": FAKE + 512}, EINVAL)):
+                     ({"q_heads": 1 << 29, "q_stride": 1 << 36}, EUNSUPPORTED), ({"window": -1}, EINVAL), ({"sinks": -1}, EINVAL), ({"sinks": 4}, EINVAL), ({"Y": FAKE + 512}, EINVAL)):
         assert attention(b=batch(max_kv=60), **kw) == want, (kw, qlin.last_error())
     need = C.c_size_t()
     long = batch(max_kv=100000, table_stride=2000, max_new=1)
