@@ -333,17 +333,23 @@ __global__ __launch_bounds__(256) void kv8_gather_kernel(const Kv8View c, uint16
     const float2 s = reinterpret_cast<const float2*>(c.scales)[block];
     const int8_t* kp = c.k + block * P * D;
     const uint4* vp = reinterpret_cast<const uint4*>(c.v + block * P * D);
-    for (int i = tid; i < D * P / 16; i += blockDim.x) {
-      const uint4 w = vp[i];
-      const int d = (16 * i) >> c.log_page;
-      uint32_t* o = reinterpret_cast<uint32_t*>(turn + d * stride + ((16 * i) & (P - 1)));
+    const auto key = [&](int i) {                            // 16 key codes of item i
+      return *reinterpret_cast<const uint4*>(kp + static_cast<size_t>(s0 + (i >> log_dp)) * D + 16 * (i & (DP - 1)));
+    };
+    const int n = (hi - lo) << log_dp;
+    const uint4 first_key = key(min(tid, n - 1));            // on its way beside the values
+    const int c0 = s0 >> 4, pieces = ((s0 + hi - lo + 15) >> 4) - c0;
+    for (int i = tid; i < D * pieces; i += blockDim.x) {
+      const int d = i / pieces, piece = c0 + i - d * pieces;
+      const uint4 w = vp[(d << (c.log_page - 4)) + piece];
+      uint32_t* o = reinterpret_cast<uint32_t*>(turn + d * stride + 16 * piece);
       o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
     }
     __syncthreads();
-    for (int i = tid; i < (hi - lo) * DP; i += blockDim.x) {
+    for (int i = tid; i < n; i += blockDim.x) {
       const int t = i >> log_dp, p = i & (DP - 1);
       const size_t row = static_cast<size_t>(q.row + (lo - q.start) + t);
-      const uint4 w = *reinterpret_cast<const uint4*>(kp + static_cast<size_t>(s0 + t) * D + 16 * p);
+      const uint4 w = i == tid ? first_key : key(i);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
       float kx[16], vx[16];
 #pragma unroll
