@@ -49,12 +49,14 @@ struct alignas(16) Tile16 {
   uint32_t held;                                            // bit s: run s has a page
 };
 
-// Schedules N products whose A operands come from LDS so that a product's operand
-// is on its way four products ahead (the compiler alone asks for it one product
-// ahead and waits: 2-3 % slower), and ends the scheduling region.
+// Schedules the N products of this block, whose A operands come from LDS, so that a
+// product's operand is on its way six products ahead, and ends the scheduling
+// region.  The compiler alone asks for it one product ahead and waits each time:
+// heads of 256, one wave to a SIMD: 4096 rows of 16 heads 230 -> 202 us; heads of
+// 128: 1046 -> 1001 us on operands of zeros, where the clock does not sink.
 template <int N>
 __device__ __forceinline__ void lookahead() {
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 6;
   __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);     // LDS reads
 #pragma unroll
   for (int i = 0; i < N - AHEAD; ++i) {
@@ -190,6 +192,8 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
         *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4)]) = codes_f16(vw[n].x, vw[n].y);
         *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4) + 8]) = codes_f16(vw[n].z, vw[n].w);
       }
+    };
+    auto put_runs = [&](Tile16<D>& to) {
       if (tid < 4) {
         const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
         to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs)};
@@ -203,6 +207,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
       load_codes(x0);
       load_pages(x0 + 1);
       put_codes(tile[0]);
+      put_runs(tile[0]);
       // (the loop inside this block, so that its waits know that the queries are there)
       // K row that this lane feeds to row `lane % 32` of a 32-token product
       const int krow = 16 * (ql >> 4) + 8 * ((ql >> 2) & 1) + 4 * ((ql >> 3) & 1) + (ql & 3);
@@ -299,6 +304,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
                                                           o[d], 0, 0, 0);
         put_codes(tile[(x - x0 + 1) & 1]);
         lookahead<4 * DT>();
+        put_runs(tile[(x - x0 + 1) & 1]);
       }
     }
     l = sum_over_32(l);
