@@ -32,7 +32,15 @@
 // rescaled) when a score exceeds it by more than kSlack, which spares the
 // cross-lane maximum and the rescaling in most tiles.
 //
-// Bound by memory: 2 D bytes a token against 4 D 16 NT matrix flops.
+// Bound by memory: 2 D bytes a token against 4 D 16 NT matrix flops.  64 ragged
+// sequences of up to 8192 tokens (8 heads of 128, 499 MB) run at 6.0 TB/s, one of
+// 131072 (269 MB) at 5.5, where a bare streaming read of the same sizes makes 7.0
+// and 6.7.  The vector units are busy 45 % of the time (conversion of the codes
+// two thirds of it); what is left is the beginning and the end of a workgroup:
+// the chain lengths -> page -> codes, and joining the waves and the splits (2, 2
+// and 4 us of the 49 us of 131072 tokens).  Tried without gain: 32 positions to a step
+// with twice the waves (64 sequences 103 -> 117 us at the time), 128 registers for
+// four waves per SIMD (103 -> 141).
 
 #include <algorithm>
 
