@@ -425,9 +425,9 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  *   overlap Q.  scale: finite, > 0.  tokens * q_heads < 2^30, seqs * kv_heads
  *   <= 2^22 (EUNSUPPORTED).
  *   workspace: conventions at the top.
- * Kernel by the rows max_new * q_heads / kv_heads of a key/value head: up to 128
- * one that holds 16 or 32 rows and splits the cache over its waves, above that
- * (from 17 rows on where there are many sequences, from 65 with head_dim 256) one
+ * Kernel by the rows max_new * q_heads / kv_heads of a key/value head: one that
+ * holds 16 or 32 rows and splits the cache over its waves up to 64 rows (16 with
+ * head_dim 256), and up to 128 (64) while there are few sequences; otherwise one
  * that holds 128 or 256 rows and shares tiles of the cache; in batches of eight
  * and more sequences each takes those that suit it.
  * Codes enter the matrix instructions as exact fp16 integers and products are

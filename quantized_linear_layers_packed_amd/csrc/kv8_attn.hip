@@ -464,7 +464,7 @@ constexpr int kMixedSeqs = 8;
 // Where the longest sequence wants the kernel for many rows, batches of eight and
 // more sequences may well hold single tokens too (prompts that join a running
 // batch): those then have a launch of the kernel for few rows of their own, which
-// costs 3 us when there are none.
+// costs 4 us when there are none.
 Kv8AttnPlan kv8_attn_plan(const Kv8AttnArgs& a) {
   Kv8AttnPlan p{};
   const int cus = device_cus();
