@@ -426,10 +426,10 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  *   <= 2^22 (EUNSUPPORTED).
  *   workspace: conventions at the top.
  * Kernel by the rows max_new * q_heads / kv_heads of a key/value head: one that
- * holds 16 or 32 rows and splits the cache over its waves up to 64 rows (16 with
- * head_dim 256), and up to 128 (64) while there are few sequences; otherwise one
- * that holds 128 or 256 rows and shares tiles of the cache; in batches of eight
- * and more sequences each takes those that suit it.
+ * holds 16 or 32 rows and splits the cache over its waves up to 64 rows (with
+ * head_dim 256 up to 16, or 32 where seqs * kv_heads >= 8); otherwise one that
+ * holds 128 or 256 rows and shares tiles of the cache; in batches of eight and
+ * more sequences each takes those that suit it.
  * Codes enter the matrix instructions as exact fp16 integers and products are
  * summed in fp32; bf16 queries are scaled to fp16 by a power of two per row (as
  * in qlin_w4_forward); softmax statistics are fp32; the weights are rounded to

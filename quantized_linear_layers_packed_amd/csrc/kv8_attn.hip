@@ -57,6 +57,7 @@ namespace {
 // Waves of a SIMD that the registers allow.
 constexpr int row_occupancy(int dim, int nt) { return dim * nt <= 128 ? 2 : 1; }
 constexpr int kMostSplits = 64;           // a lane each when they are joined
+constexpr int kMostManySplits = 256;      // of the kernel for many rows: joined by a kernel of its own
 // 16 NT query rows as B operands: lane (q, g), slice (u, e) holds dimensions
 // 64 u + 16 g + 8 e .. + 7 of row q.  bf16 rows are scaled by a power of two into
 // fp16's range; *mul is what undoes it.
@@ -368,19 +369,24 @@ void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
 }
 
 // 16-row column tiles per wave of the kernel for few rows, 0 for the kernel for
-// many rows.  Up to 128 rows one column tile with a workgroup for each 16 rows is
-// fastest while these are too few to fill the device, although each reads the
-// cache (64 rows over 32768 tokens of 4 heads: 27 us, with two column tiles 36, the
-// kernel for many rows 51); then two column tiles (64 sequences of 2048 tokens, 64
-// rows each: 66, 55 and 81 us; 128 rows each: 116, 93 and 85 us).  Heads of 256
-// dimensions have registers for one column tile.
+// many rows.  One column tile with a workgroup for each 16 rows reads the cache
+// once for each of them, and is fastest while these do not fill the device (one,
+// two column tiles, many rows; heads of 128: 64 rows over 32768 tokens of 4 heads
+// 28, 36 and 32 us, 32 rows over 16 sequences of 2048 of 8 heads 19, 28 and 49);
+// then two column tiles (64 sequences of 2048, 64 rows each: 119, 99 and 151 us),
+// for up to 32 rows over long sequences already where a quarter is full (32 of
+// 8192 of 2 heads: 47, 35 and 35 us at half).  From 65 rows the kernel for many is
+// as good or better (128 rows over 32768 tokens of 8 heads: 58, 51 and 49 us).
+// Heads of 256 dimensions have registers for one column tile, which pays for up to
+// 32 rows (64 sequences of 4096 of 2 heads: 87 against 110 us, 33 to 48 rows 144
+// against 112) from eight key/value heads of sequences on (one sequence of 32768
+// with 8 heads 47 against 62, with 2 heads 44 against 29).
 int rows_nt(const Kv8AttnArgs& a, int cus) {
   const long long rows = static_cast<long long>(a.c.max_new) * a.group, per_tile = static_cast<long long>(a.c.seqs) * a.c.heads;
   const long long units = per_tile * ((rows + 15) / 16);
   if (rows <= 16) return 1;
-  if (a.c.dim > 128) return rows <= 64 && units <= 2LL * cus ? 1 : 0;
-  if (rows <= 64) return units <= (rows <= 32 ? cus / 4 : cus) ? 1 : 2;
-  if (rows <= 128) return units <= cus / 2 ? 1 : per_tile * ((rows + 31) / 32) <= cus ? 2 : 0;
+  if (a.c.dim > 128) return rows <= 32 && per_tile >= 8 ? 1 : 0;
+  if (rows <= 64) return units <= (rows <= 32 && a.c.max_kv > 4096 ? cus / 4 : cus) ? 1 : 2;
   return 0;
 }
 
@@ -423,11 +429,13 @@ size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
   // beginning and end, and joining splits, cost in steps.  One workgroup to a
   // compute unit, also where two would fit: twice the splits cost more than they
   // hide (131072 tokens 50 -> 59 us).  Row tiles of a prompt differ in length and
-  // are not split once there is one for every workgroup that fits.
+  // are not split once there is one for every workgroup that fits.  Up to 256 splits
+  // for many rows (32 rows of 8 heads over 131072 tokens 70 us with 64, 39 with 256).
   const long long slots = static_cast<long long>(cus) * (nt ? 1 : kv8_prompt_resident(a->c.dim));
-  const long long steps = nt ? a->waves : 1, alone = 3, split = nt ? 5 : 6;
+  const long long steps = nt ? a->waves : 1, alone = 3, split = 5;
+  const long long most_splits = nt ? kMostSplits : kMostManySplits;
   long long splits = 1, best = -1;
-  for (long long n = 1; (nt || units < slots) && n <= kMostSplits && n <= std::max<long long>(tiles / 2, 1); ++n) {
+  for (long long n = 1; (nt || units < slots) && n <= most_splits && n <= std::max<long long>(tiles / 2, 1); ++n) {
     const long long each = ((tiles + n - 1) / n + steps - 1) / steps;
     const long long cost = ((units * n + slots - 1) / slots) * (each + (n > 1 ? split : alone));
     if (best < 0 || cost < best) best = cost, splits = n;

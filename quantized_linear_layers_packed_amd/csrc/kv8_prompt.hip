@@ -100,6 +100,10 @@ struct RowTile {
 template <int D>
 constexpr int kPromptSlot = kPromptWaves<D> * 64 * (D / 2 + 2);
 
+// Threads of a workgroup that joins splits, SHARE waves to a task.
+template <int SHARE>
+constexpr int kJoinThreads = SHARE > 4 ? 64 * SHARE : 256;
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8_prompt_kernel(const Kv8AttnArgs a) {
   constexpr int W = kPromptWaves<D>, NT = 64 * W, ROWS = 32 * W, DT = D / 32, KS = D / 16;
@@ -346,48 +350,70 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
   }
 }
 
-// Joins the splits of row tiles, in their order: a wave per row tile, wave of it
-// and group of four sums, spread over the whole device (one workgroup joining 64
-// splits of 256 rows would read 9 MB by itself).
-template <int D, bool BF16>
-__global__ __launch_bounds__(256) void kv8_prompt_join_kernel(const Kv8AttnArgs a) {
+// Joins the splits of row tiles, in their order, spread over the whole device (one
+// workgroup joining 64 splits of 256 rows would read 9 MB by itself): a row tile's
+// wave and a group of four of its sums are a task, of SHARE waves that take
+// consecutive splits each.  What bounds it is the latency of its loads: with one
+// wave to a task 64 splits took 24.5 us, with sixteen, whose loads all leave at
+// once, 5 us.
+template <int D, int SHARE, bool BF16>
+__global__ __launch_bounds__(kJoinThreads<SHARE>) void kv8_prompt_join_kernel(const Kv8AttnArgs a) {
   constexpr int GROUPS = D / 8, AHEAD = 8;
-  const int lane = threadIdx.x & 63, h = lane >> 5, ql = lane & 31;
-  const int task = blockIdx.y * 4 + (threadIdx.x >> 6), wv = task / GROUPS, group = task % GROUPS;
+  const int lane = threadIdx.x & 63, h = lane >> 5, ql = lane & 31, wave = threadIdx.x >> 6, member = wave % SHARE;
+  const int task = blockIdx.y * (kJoinThreads<SHARE> / 64 / SHARE) + wave / SHARE, wv = task / GROUPS, group = task % GROUPS;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads, b = a.by_row_tiles(unit);
   const Kv8Seq seq = kv8_seq(a.c, b);
   const int rows = seq.count * a.group, r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * RowTile<D>::ROWS;
   if (r0 >= rows || rows < a.least_rows || rows > a.most_rows) return;
   const RowTile<D> rt(a, seq, rows, r0);
-  if (rt.used == 1) return;
+  if (rt.used == 1 || 32 * wv >= rt.nrows) return;          // (the same for all of a task)
   const float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * kPromptSlot<D> + wv * 64 * (D / 2 + 2) + lane;
-  const float* stats = part + 64 * (D / 2);
-  float m = kNone;
-  for (int k = 0; k < rt.used; k += AHEAD) {
-    float v[AHEAD];
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) v[j] = stats[static_cast<size_t>(min(k + j, rt.used - 1)) * kPromptSlot<D>];
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) m = fmaxf(m, v[j]);
-  }
-  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < rt.used; k += AHEAD) {
+  const int each = (rt.used + SHARE - 1) / SHARE, k1 = min(rt.used, (member + 1) * each);
+  float m = kNone, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = member * each; k < k1; k += AHEAD) {
     float ref[AHEAD], sum[AHEAD], v[AHEAD][4];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      const size_t at = static_cast<size_t>(min(k + j, rt.used - 1)) * kPromptSlot<D>;
-      ref[j] = stats[at];
-      sum[j] = stats[at + 64];
+      const float* at = part + static_cast<size_t>(min(k + j, k1 - 1)) * kPromptSlot<D>;
+      ref[j] = at[64 * (D / 2)];
+      sum[j] = at[64 * (D / 2 + 1)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = part[at + 64 * (4 * group + i)];
+      for (int i = 0; i < 4; ++i) v[j][i] = at[64 * (4 * group + i)];
     }
+    float next = m;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) next = fmaxf(next, ref[j]);
+    const float f = __builtin_amdgcn_exp2f(m - next);
+    m = next;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= f;
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      if (k + j >= rt.used) break;
-      const float f = __builtin_amdgcn_exp2f(ref[j] - m);
-      l = fmaf(sum[j], f, l);
+      if (k + j >= k1) break;
+      const float g = __builtin_amdgcn_exp2f(ref[j] - m);
+      l = fmaf(sum[j], g, l);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[j][i], f, o[i]);
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[j][i], g, o[i]);
+    }
+  }
+  if constexpr (SHARE > 1) {
+    __shared__ float held[SHARE][6][64];
+    held[member][0][lane] = m;
+    held[member][1][lane] = l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) held[member][2 + i][lane] = o[i];
+    __syncthreads();
+    if (member) return;
+#pragma unroll
+    for (int k = 1; k < SHARE; ++k) m = fmaxf(m, held[k][0][lane]);
+    l = o[0] = o[1] = o[2] = o[3] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < SHARE; ++k) {
+      const float g = __builtin_amdgcn_exp2f(held[k][0][lane] - m);
+      l = fmaf(held[k][1][lane], g, l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(held[k][2 + i][lane], g, o[i]);
     }
   }
   if (32 * wv + ql >= rt.nrows) return;
@@ -397,17 +423,23 @@ __global__ __launch_bounds__(256) void kv8_prompt_join_kernel(const Kv8AttnArgs 
   *reinterpret_cast<uint2*>(y) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
 }
 
+template <int D, int SHARE>
+void join_launch(const Kv8AttnArgs& a, int dtype, unsigned units, hipStream_t stream) {
+  constexpr int kTasks = kPromptWaves<D> * (D / 8);
+  const dim3 grid(units, kTasks / (kJoinThreads<SHARE> / 64 / SHARE)), block(kJoinThreads<SHARE>);
+  const auto fn = dtype == QLIN_BF16 ? kv8_prompt_join_kernel<D, SHARE, true> : kv8_prompt_join_kernel<D, SHARE, false>;
+  hipLaunchKernelGGL(fn, grid, block, 0, stream, a);
+}
+
 template <int D>
 void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * kPromptWaves<D>);
   const size_t lds = 2 * sizeof(Tile16<D>);
   const auto fn = dtype == QLIN_BF16 ? kv8_prompt_kernel<D, true> : kv8_prompt_kernel<D, false>;
   hipLaunchKernelGGL(fn, grid, block, lds, stream, a);
-  if (a.splits > 1) {
-    const dim3 tasks(grid.x, kPromptWaves<D> * (D / 8) / 4);
-    const auto join = dtype == QLIN_BF16 ? kv8_prompt_join_kernel<D, true> : kv8_prompt_join_kernel<D, false>;
-    hipLaunchKernelGGL(join, tasks, dim3(256), 0, stream, a);
-  }
+  if (a.splits > 32) join_launch<D, 16>(a, dtype, grid.x, stream);
+  else if (a.splits > 8) join_launch<D, 4>(a, dtype, grid.x, stream);
+  else if (a.splits > 1) join_launch<D, 1>(a, dtype, grid.x, stream);
 }
 
 }  // namespace

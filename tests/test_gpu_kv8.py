@@ -368,6 +368,22 @@ def test_every_kernel_choice_by_rows(D, rows):
         check_attention(s, 4, F16)
 
 
+@pytest.mark.parametrize("dtype,D,P,G,new,kv,window,sinks", [
+    (F16, 128, 64, 8, [30], [33000], 0, 0),                             # a row tile split more than 64 times
+    (BF16, 64, 16, 8, [13], [20011], 0, 0),
+    (F16, 256, 32, 4, [25, 20], [20000, 70], 0, 0),                     # the second of one split
+    (BF16, 256, 128, 8, [33, 5], [3000, 9000], 0, 0),
+    (F16, 64, 64, 2, [200, 40, 1], [9000, 3000, 8000], 2000, 100),
+    (BF16, 128, 32, 1, [70, 0, 3, 1, 200, 1, 1, 2], [12000, 9, 3, 5000, 200, 1, 77, 1600], 0, 0),
+])
+def test_few_rows_of_long_sequences_in_many_splits(dtype, D, P, G, new, kv, window, sinks):
+    s = Setup(23, D, P, 1, new, kv)
+    Q = s.rng.standard_normal((s.T, G, D))
+    first = back(check_attention(s, G, dtype, Q=Q, window=window, sinks=sinks))
+    for _ in range(3):
+        assert np.array_equal(back(run_attention(s, G, dtype, Q=Q, window=window, sinks=sinks)[0]), first)
+
+
 def test_attention_splits_are_deterministic_and_reuse_their_workspace():
     torch = torch_cuda()
     s = Setup(17, 128, 64, 2, [1, 1], [9000, 4100])
