@@ -433,9 +433,9 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  * Codes enter the matrix instructions as exact fp16 integers and products are
  * summed in fp32; bf16 queries are scaled to fp16 by a power of two per row (as
  * in qlin_w4_forward); softmax statistics are fp32; the weights are rounded to
- * fp16 relative to their row's running maximum.  Long sequences are
- * split over workgroups and joined in a fixed order: results do not depend on
- * timing. */
+ * fp16, by 2^-11 of themselves or 2^-32 of their row's largest, whichever is
+ * more.  Long sequences are split over workgroups and joined in a fixed order:
+ * results do not depend on timing. */
 qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
                                const void* Q, int dtype, int q_heads, int64_t q_stride,
                                float scale, int window, int sinks, void* Y,

@@ -23,10 +23,10 @@
 // Codes become exact fp16 integers (one v_perm for two codes and one packed
 // subtraction).  The key scale multiplies the fp32 scores.  The value scale t_j
 // goes into the weights, in the exponent: p'_qj = p_qj t_j 2^-m_q, with the
-// reference m_q near the row's maximum of score + log2 t_j, so the largest p' are
-// near 1 and round to fp16 with 11 bits, and what falls below 2^-24 is below the
-// rounding of the largest.  O[q] = sum p' (codes of v) / sum p' / t, the sum of
-// weights in fp32.
+// reference m_q somewhat below the row's maximum of score + log2 t_j, so the largest
+// p' are 2^7 to 2^15: p' down to 2^-14 round to fp16 with 11 bits, smaller ones to
+// a multiple of 2^-24.  O[q] = sum p' (codes of v) / sum p' / t, the sum of weights
+// in fp32.
 //
 // The reference only has to be near the maximum: it moves (and the sums are
 // rescaled) when a score exceeds it by more than kSlack, which spares the
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
         // every position of the tile visible to every row, and every page there
         const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && !__any(!here);
         const float vs = s.y < kLeastScale ? kLeastScale : s.y;                // NaN stays
-        const float lv = __log2f(vs), iv = 1.0f / vs;
+        const float lv = __log2f(vs), iv = kSumUnit / vs;
         h8_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
           if (__any(top > m[n] + kSlack)) {
             const float was = m[n];
             const float high = max_over_g(top);
-            m[n] = high > was + kSlack ? high : was;           // by the row's own scores alone
+            m[n] = high > was + kSlack ? high - kHead : was;           // by the row's own scores alone
             const float f = __builtin_amdgcn_exp2f(was - m[n]);
             l[n] *= f;
 #pragma unroll
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
           y1 += sums[w][rr][d + 1];
         }
         if (used == 1) {
-          const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+          const float inv = by_weights(total);
           const int row = r0 + r, t = a.by_group(row), h = head * G + row - t * G;
           *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
         } else {
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
       const float f = __builtin_amdgcn_exp2f(mine.x - wave_max(mine.x));
       weigh[r * kMostSplits + lane] = f;
       const float total = wave_sum(mine.y * f);
-      if (lane == 0) factor[r] = total == 0.0f ? 0.0f : 1.0f / total;
+      if (lane == 0) factor[r] = by_weights(total);
     }
     __syncthreads();
     for (int i = tid; i < nrows * (D / 2); i += 64 * W) {

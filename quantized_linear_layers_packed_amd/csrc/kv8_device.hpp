@@ -8,7 +8,17 @@
 namespace qlin {
 
 constexpr int kTile = 64;                      // positions per step of a wave or workgroup
-constexpr float kSlack = 8.0f;                 // scores may exceed the row's reference by 2^8
+// A row's reference is set kHead below its largest score and moves when a score
+// exceeds it by more than kSlack.  The weights 2^(score - reference) are rounded to
+// fp16: the largest is then 2^7 at least and no weight passes 2^15 (of 65504), so
+// that weights down to 2^-21 of the largest keep 11 bits and those below lose 2^-32
+// of it at most.  The tail of a long sequence lives there: 131003 tokens of
+// 2^-20.6 each beside one large weight came out 2 % off with weights of up to 1.
+constexpr float kHead = 7.0f;
+constexpr float kSlack = kHead + 8.0f;
+// The sum of weights is held in this unit, for its headroom: with kLeastScale it
+// stays below 2^(15 + 100 - 12 + 24) for 2^24 tokens.
+constexpr float kSumUnit = 2.4414062e-4f;      // 2^-12
 constexpr float kNone = -1.0e30f;              // reference of a row that has seen nothing
 constexpr float kLeastScale = 7.8886091e-31f;  // 2^-100: smaller value scales (0 among them) count as that
 
@@ -152,6 +162,10 @@ __device__ __forceinline__ h8_t chunk_f16(const uint4& w, int e) {
     q[j] = static_cast<_Float16>(ldexpf(bf16_bits_to_f32(static_cast<uint16_t>(x[j >> 1] >> (16 * (j & 1)))), -e));
   return q;
 }
+
+// What sums of weighted codes are multiplied by, from the sum of weights (in its
+// unit): rows that see nothing give zeros.
+__device__ __forceinline__ float by_weights(float total) { return total == 0.0f ? 0.0f : kSumUnit / total; }
 
 // Values rounded to the output type, two to a word.
 template <bool BF16>

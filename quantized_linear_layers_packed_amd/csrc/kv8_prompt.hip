@@ -44,7 +44,7 @@ template <int D>
 constexpr int kPromptOccupancy = D > 128 ? 1 : 2;
 
 // A run of 16 tokens of a tile: its key scale, log2 and reciprocal of its value
-// scale.
+// scale (the latter in the unit of the sum of weights).
 struct alignas(16) Run {
   float key, lv, iv;
 };
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     auto put_runs = [&](Tile16<D>& to) {
       if (tid < 4) {
         const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
-        to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs)};
+        to.run[tid] = Run{scale2.x, __log2f(vs), kSumUnit * __builtin_amdgcn_rcpf(vs)};
       }
       const uint32_t held = static_cast<uint32_t>(__ballot(held_next)) & 15u;  // lanes 0 .. 3 of wave 0: the four runs
       if (tid == 0) to.held = held;
@@ -273,7 +273,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
         }
         if (__any(top > m + kSlack)) {
           const float high = max_over_32(top), was = m;
-          m = high > was + kSlack ? high : was;               // by the row's own scores alone
+          m = high > was + kSlack ? high - kHead : was;               // by the row's own scores alone
           const float f = __builtin_amdgcn_exp2f(was - m);
           l *= f;
 #pragma unroll
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
       part[64 * 16 * DT] = m;
       part[64 * 16 * DT + 64] = l;
     } else if (mine) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = by_weights(l);
       int again = tid;
       asm volatile("" : "+v"(again));                       // (nothing of the address to be held through the loop)
       uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + ((again & 32) >> 3);
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(kJoinThreads<SHARE>) void kv8_prompt_join_kernel(co
   }
   if (32 * wv + ql >= rt.nrows) return;
   const int r = r0 + 32 * wv + ql, t = a.by_group(r), hq = head * a.group + r - t * a.group;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = by_weights(l);
   uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + 32 * (group >> 2) + 8 * (group & 3) + 4 * h;
   *reinterpret_cast<uint2*>(y) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
 }
