@@ -419,7 +419,8 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  * window or j < sinks (a sliding window and a few first tokens that stay
  * visible; window 0: all of them, sinks then has to be 0).  Query heads share
  * key/value heads in runs of q_heads / kv_heads.  Queries that see nothing give
- * zeros.
+ * zeros.  Scores are held in fp32 (times log2(e)); queries whose visible scores are
+ * all below its range, or one of them above it or NaN, give NaN.
  *   Q device, tokens q_stride elements apart (a multiple of 8), Y device
  *   [tokens][q_heads][head_dim], both of dtype QLIN_F16 or QLIN_BF16; Y must not
  *   overlap Q.  scale: finite, > 0.  tokens * q_heads < 2^30, seqs * kv_heads

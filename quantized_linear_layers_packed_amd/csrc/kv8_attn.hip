@@ -223,7 +223,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
         for (int n = 0; n < NT; ++n) {
           const float c = s.x * cq[n];
           const uint32_t seen = full ? 0xFFFFu : visible_bits<16>(j0, pos[n], low[n], a.sinks, here);
-          float top = kNone;
+          float top = seen != 0 ? kLowest : kNone;
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -308,7 +308,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
           y1 += sums[w][rr][d + 1];
         }
         if (used == 1) {
-          const float inv = by_weights(total);
+          const float inv = by_weights(total, ref);
           const int row = r0 + r, t = a.by_group(row), h = head * G + row - t * G;
           *reinterpret_cast<uint32_t*>(a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + h) * D + d) = pack2<BF16>(y0 * inv, y1 * inv);
         } else {
@@ -328,10 +328,10 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
     float* factor = weigh + 16 * NT * kMostSplits;
     for (int r = wv; r < nrows; r += W) {
       const float2 mine = lane < used ? sk_load2(first + lane * kPartial<D, NT> + 16 * NT * D + 2 * r) : make_float2(kNone, 0.0f);
-      const float f = __builtin_amdgcn_exp2f(mine.x - wave_max(mine.x));
+      const float ref = wave_max(mine.x), f = __builtin_amdgcn_exp2f(mine.x - ref);
       weigh[r * kMostSplits + lane] = f;
       const float total = wave_sum(mine.y * f);
-      if (lane == 0) factor[r] = by_weights(total);
+      if (lane == 0) factor[r] = by_weights(total, ref);
     }
     __syncthreads();
     for (int i = tid; i < nrows * (D / 2); i += 64 * W) {

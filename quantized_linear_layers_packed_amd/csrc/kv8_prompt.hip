@@ -253,6 +253,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
         const uint32_t held = __builtin_amdgcn_readfirstlane(now.held);
         const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && held == 15u;
         uint32_t seen[4];                                     // bit i of run s: this lane's token i
+        float top = kLowest;
         if (!full) {
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -261,9 +262,9 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
             for (int i = 0; i < 8; ++i)
               st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : -INFINITY;
           }
+          top = (seen[0] | seen[1] | seen[2] | seen[3]) != 0 ? kLowest : kNone;
         }
         // run s: values st[s / 2][8 (s % 2) .. + 7]
-        float top = kNone;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           float mx = st[s >> 1][8 * (s & 1)];
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
       part[64 * 16 * DT] = m;
       part[64 * 16 * DT + 64] = l;
     } else if (mine) {
-      const float inv = by_weights(l);
+      const float inv = by_weights(l, m);
       int again = tid;
       asm volatile("" : "+v"(again));                       // (nothing of the address to be held through the loop)
       uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + ((again & 32) >> 3);
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(kJoinThreads<SHARE>) void kv8_prompt_join_kernel(co
   }
   if (32 * wv + ql >= rt.nrows) return;
   const int r = r0 + 32 * wv + ql, t = a.by_group(r), hq = head * a.group + r - t * a.group;
-  const float inv = by_weights(l);
+  const float inv = by_weights(l, m);
   uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + 32 * (group >> 2) + 8 * (group & 3) + 4 * h;
   *reinterpret_cast<uint2*>(y) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
 }

@@ -117,3 +117,35 @@ def test_many_tokens_without_values_do_not_overflow_the_sum_of_weights(call):
     scales = np.where(np.arange(L // P) * P >= 131072, 1.0, 0.0)
     s = Shared(D, P, L, seqs, k, v, 0.1, scales)
     s.check(q(1.0 / LOG2E), G, F16)
+
+
+def winner_takes_all(D, key_scale):
+    """5003 cached tokens whose keys have codes -127 .. -64 in the one dimension that the query sees, but token 2400's -1."""
+    L = 5003
+    codes = -64 - np.arange(L) % 64
+    codes[2400] = -1
+    k, q = by_first_dimension(D, codes)
+    v = (np.arange(L)[:, None] % 97 + np.arange(D) % 23).astype(np.int8)
+    return L, k, v, key_scale, q
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("dtype,key_scale,x", [(BF16, 2.0 ** 60, 2.0 ** 50), (F16, 2.0 ** 100, 2.0 ** 15), (BF16, 2.0, 2.0 ** 118)])
+def test_scores_far_below_zero_still_have_a_largest(call, dtype, key_scale, x):
+    """Scores from -2^110 or -2^115 or -2^119 down: the row is its largest one's value, not zeros as if it saw nothing."""
+    D, G, seqs = CALLS[call]
+    say(f"kv8 attention, scores of -{key_scale * x:.1e}: {call}")
+    L, k, v, key_scale, q = winner_takes_all(D, key_scale)
+    Y, _ = Shared(D, 64, L, seqs, k, v, key_scale, np.ones(-(-L // 64))).run(q(x), G, dtype)
+    assert np.array_equal(Y, np.broadcast_to(v[2400].astype(np.float64), Y.shape))
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("x", [2.0 ** 100, np.inf, -2.0 ** 100, -np.inf])
+def test_scores_past_the_range_of_fp32_give_nan(call, x):
+    """All scores -inf (or +inf) in fp32: no weights can be formed, and the row says so."""
+    D, G, seqs = CALLS[call]
+    say(f"kv8 attention, scores of -{x} 2^100: {call}")
+    L, k, v, key_scale, q = winner_takes_all(D, 2.0 ** 100)
+    Y, _ = Shared(D, 64, L, seqs, k, v, key_scale, np.ones(-(-L // 64))).run(q(x), G, BF16)
+    assert np.isnan(Y).all()
