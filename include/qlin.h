@@ -423,7 +423,7 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  * all below its range, or one of them above it or NaN, give NaN.
  *   Q device, tokens q_stride elements apart (a multiple of 8), Y device
  *   [tokens][q_heads][head_dim], both of dtype QLIN_F16 or QLIN_BF16; Y must not
- *   overlap Q.  scale: finite, > 0.  tokens * q_heads < 2^30, seqs * kv_heads
+ *   overlap Q.  scale: > 0, scale * log2(e) finite in fp32.  tokens * q_heads < 2^30, seqs * kv_heads
  *   <= 2^22 (EUNSUPPORTED).
  *   workspace: conventions at the top.
  * Kernel by the rows max_new * q_heads / kv_heads of a key/value head: one that

@@ -556,7 +556,8 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
   QLIN_TRY(kv8_attn_args(fn, cache, batch, q_heads, window, sinks, false, &a, &plan, &total));
   QLIN_TRY(kv8_check_dtype(fn, dtype));
   if (!Q || !Y) return fail(QLIN_EINVAL, std::string(fn) + ": NULL Q or Y");
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QLIN_EINVAL, std::string(fn) + ": scale must be finite and positive");
+  if (!(scale > 0.0f) || !std::isfinite(a.scale))
+    return fail(QLIN_EINVAL, std::string(fn) + ": scale and scale * log2(e) must be finite and positive");
   QLIN_TRY(need_aligned(fn, "Q", Q));
   QLIN_TRY(need_aligned(fn, "Y", Y));
   QLIN_TRY(kv8_check_rows(fn, "q_stride", a.c.tokens, q_heads, a.c.dim, q_stride));
