@@ -258,6 +258,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             seen[s] = visible_bits<8>(base + 16 * s + 8 * h, pos, low, a.sinks, (held >> s) & 1u);
+            c[s] = seen[s] != 0 ? c[s] : 0.0f;                // (a hidden page's scale may be below 0: -inf must not turn)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : -INFINITY;

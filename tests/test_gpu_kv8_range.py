@@ -5,7 +5,7 @@ import pytest
 
 from quantized_linear_layers_packed_amd import qlin
 from tests.gpu_util import say, torch_cuda, workspace
-from tests.test_gpu_kv8 import back, to16
+from tests.test_gpu_kv8 import Setup, back, run_attention, to16
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +149,22 @@ def test_scores_past_the_range_of_fp32_give_nan(call, x):
     L, k, v, key_scale, q = winner_takes_all(D, 2.0 ** 100)
     Y, _ = Shared(D, 64, L, seqs, k, v, key_scale, np.ones(-(-L // 64))).run(q(x), G, BF16)
     assert np.isnan(Y).all()
+
+
+@pytest.mark.parametrize("new,window", [(1, 64), (60, 64), (1, 0), (60, 0)])
+@pytest.mark.parametrize("garbage", [np.nan, np.inf, -np.inf, -3e38, -1.0, 0.0, 1e-39, 1e-31])
+def test_scales_of_hidden_pages_may_be_anything(new, window, garbage):
+    """Pages outside the window, and those of the pool that table entries of -1 stand in for, do not reach a result."""
+    say(f"kv8 attention, hidden scales of {garbage}: new={new} window={window}")
+    P, kv = 16, 400
+    s = Setup(31, 64, P, 1, [new], [kv])
+    s.table[s.table == 0] = next(p for p in range(1, len(s.k)) if p not in s.table)   # page 0 stands in for -1
+    s.table[0, 5:12] = -1
+    s.upload()
+    Q = np.full((new, 4, 64), 0.5)
+    clean = back(run_attention(s, 4, F16, window=window, Q=Q)[0])
+    s.scales[[p for p in range(len(s.k)) if p not in s.table]] = garbage
+    if window:
+        s.scales[s.table[0, 12:(kv - new - window) // P]] = garbage
+    s.upload()
+    assert np.isfinite(clean).all() and np.array_equal(back(run_attention(s, 4, F16, window=window, Q=Q)[0]), clean)
