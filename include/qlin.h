@@ -338,6 +338,9 @@ qlin_status qlin_f16_gemm(const uint16_t* X, const uint16_t* W, int M, int N, in
  *   scales  fp32 [num_pages][kv_heads][2]                    (K scale, V scale)
  *
  * Pages need no initialization: the first append into a page starts its scales.
+ * Scales that are written otherwise have to be at least 0, and those of values 0
+ * (with codes of 0) or at least 2^-80, as append keeps them.  Beside values with
+ * scales above 2^20, tokens of scales 2^100 times smaller may lose their weight.
  * head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; num_pages * kv_heads
  * below 2^31 (EUNSUPPORTED otherwise).  Offsets into the pool are 64-bit.     */
 typedef struct {
@@ -391,8 +394,8 @@ qlin_status qlin_kv8_sizes(int num_pages, int kv_heads, int head_dim, int page_s
  * page's new tokens; s = a / 127, or the page's scale s_old if it already holds
  * earlier tokens of the sequence and s_old is larger; codes
  * clamp(rint(x * (1 / s)), -127, 127).  Where s > s_old the earlier tokens' codes
- * become rint(q * (s_old * (1 / s))).  s below 2^-126 counts as 0, codes 0.  A
- * NaN or infinity among the page's values makes its scale NaN (until the page
+ * become rint(q * (s_old * (1 / s))).  s below 2^-126 (keys) or 2^-80 (values)
+ * counts as 0, codes 0.  A NaN or infinity among the page's values makes its scale NaN (until the page
  * is started anew): whoever sees a token of it gets NaN, nobody else does.
  * No two sequences of a call may store into the same page.  Requirements: seqs,
  * tokens, q_heads, max_new, max_kv > 0, q_heads a multiple of kv_heads (ignored

@@ -8,7 +8,7 @@ sequence b owns tokens offsets[b] .. offsets[b+1]-1, the last of its kv_lens[b].
 Append, per page and head (K and V apart): s = max |new| / 127, or the old scale
 if the page already holds earlier tokens and it is larger; earlier codes become
 rint(q * (s_old * (1/s))) where s grew; new codes clamp(rint(x * (1/s)), +-127).
-Scales below 2^-126 are 0 (codes 0); a value that is not finite makes the scale NaN.
+Scales below 2^-126 (K) or 2^-80 (V) are 0 (codes 0); a value that is not finite makes the scale NaN.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
 """
@@ -41,13 +41,13 @@ def _quantize(x: np.ndarray, inv: np.float32) -> np.ndarray:
         return np.clip(np.rint(x.astype(F) * inv), F(-127), F(127))
 
 
-def _store(fresh: np.ndarray, old_codes: np.ndarray, s_old: np.float32):
+def _store(fresh: np.ndarray, old_codes: np.ndarray, s_old: np.float32, least: float):
     """fresh fp32 [t][dim], old_codes int8 [olds][dim]: (scale, all codes, whether the codes mean anything)."""
     a = np.max(np.abs(fresh)) if np.isfinite(fresh).all() else F(np.nan)
     s = F(a) / F(127)
     if len(old_codes):
         s = F(np.nan) if np.isnan(s) or np.isnan(s_old) else max(s, F(s_old))
-    if s < F(2.0) ** -126:
+    if s < F(least):
         s = F(0)
     if np.isnan(s):
         return s, np.zeros((len(old_codes) + len(fresh), fresh.shape[1]), np.int8), False
@@ -79,11 +79,11 @@ def append(k_codes, v_codes, scales, offsets, kv_lens, table, Q, K, V, cos, sin,
                 t = slice(lo - (m - n), hi - (m - n))
                 for h in range(H):
                     fresh_k = np.stack([r[h] for r in rotated[t]])
-                    s, codes, _ = _store(fresh_k, k_codes[page, h, :olds], scales[page, h, 0])
+                    s, codes, _ = _store(fresh_k, k_codes[page, h, :olds], scales[page, h, 0], 2.0 ** -126)
                     scales[page, h, 0] = s
                     k_codes[page, h, :olds + hi - lo] = codes
                     fresh_v = V[row:row + n][t][:, h]
-                    s, codes, _ = _store(fresh_v, v_codes[page, h, :, :olds].T, scales[page, h, 1])
+                    s, codes, _ = _store(fresh_v, v_codes[page, h, :, :olds].T, scales[page, h, 1], 2.0 ** -80)
                     scales[page, h, 1] = s
                     v_codes[page, h, :, :olds + hi - lo] = codes.T
             lo = hi

@@ -129,16 +129,17 @@ __device__ __forceinline__ uint32_t low_bytes(int n) {
 
 // The scale of a page after the call, its reciprocal for new values and the
 // factor for earlier codes.  most: the largest magnitude bits of the new values
-// (they order like the magnitudes, infinities and NaN last).
+// (they order like the magnitudes, infinities and NaN last).  least: smaller scales
+// are 0.
 struct PageScale {
   float s, inv, r;
   bool grew;
 };
-__device__ __forceinline__ PageScale page_scale(uint32_t most, bool earlier, float s_old) {
+__device__ __forceinline__ PageScale page_scale(uint32_t most, bool earlier, float s_old, float least) {
   PageScale p;
   const float fresh = __fdiv_rn(bitcast<float>(most), 127.0f);
   p.s = earlier ? fmaxf(fresh, s_old) : fresh;
-  if (p.s < 1.17549435e-38f) p.s = 0.0f;
+  if (p.s < least) p.s = 0.0f;
   if (most >= 0x7F800000u || (earlier && s_old != s_old)) p.s = __builtin_nanf("");
   p.inv = p.s > 0.0f ? __fdiv_rn(1.0f, p.s) : 0.0f;
   p.r = s_old * p.inv;
@@ -197,7 +198,7 @@ __device__ __forceinline__ void store_page(const Kv8AppendArgs& a, const Kv8Seq&
     mk = max(mk, red[0][w]);
     mv = max(mv, red[1][w]);
   }
-  const PageScale sk = page_scale(mk, olds > 0, s_old.x), sv = page_scale(mv, olds > 0, s_old.y);
+  const PageScale sk = page_scale(mk, olds > 0, s_old.x, 1.17549435e-38f), sv = page_scale(mv, olds > 0, s_old.y, kLeastScale);
   if (tid == 0) *sp = make_float2(sk.s, sv.s);
 
   // keys, and the values' codes into the transposed page in LDS

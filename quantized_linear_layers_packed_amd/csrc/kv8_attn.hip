@@ -217,7 +217,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
         // every position of the tile visible to every row, and every page there
         const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && !__any(!here);
         const float vs = s.y < kLeastScale ? kLeastScale : s.y;                // NaN stays
-        const float lv = __log2f(vs), iv = kSumUnit / vs;
+        const float lv = __log2f(vs), iv = 1.0f / vs;
         h8_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {

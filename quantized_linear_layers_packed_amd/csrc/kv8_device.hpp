@@ -16,16 +16,10 @@ constexpr int kTile = 64;                      // positions per step of a wave o
 // 2^-20.6 each beside one large weight came out 2 % off with weights of up to 1.
 constexpr float kHead = 7.0f;
 constexpr float kSlack = kHead + 8.0f;
-// The sum of weights is held in this unit, for its headroom: with kLeastScale it
-// stays below 2^(15 + 100 - 12 + 24) for 2^24 tokens.
-constexpr float kSumUnit = 2.4414062e-4f;      // 2^-12
 // References of rows that have seen nothing, and nothing but scores below all that
 // fp32 holds: any finite score moves both.
 constexpr float kNone = -3.40282347e38f;
 constexpr float kLowest = -3.4e38f;
-constexpr float kLeastScale = 7.8886091e-31f;  // 2^-100: smaller value scales (0 among them) count as that
-
-constexpr float kLeastFactor = 1.0e-30f;       // smaller score factors (0 among them) count as that: no score changes
 
 // 8 codes (two words) as 8 fp16 integers, in order: byte + 128 into the low
 // mantissa of 1024, minus 1152.
@@ -166,11 +160,11 @@ __device__ __forceinline__ h8_t chunk_f16(const uint4& w, int e) {
   return q;
 }
 
-// What sums of weighted codes are multiplied by, from the sum of weights (in its
-// unit) and the row's reference: rows that see nothing give zeros, rows that see
-// scores of -inf alone NaN.
+// What sums of weighted codes are multiplied by, from the sum of weights and the
+// row's reference: rows that see nothing give zeros, rows that see scores of -inf
+// alone NaN.
 __device__ __forceinline__ float by_weights(float total, float ref) {
-  return total == 0.0f ? (ref > kNone ? __builtin_nanf("") : 0.0f) : kSumUnit / total;
+  return total == 0.0f ? (ref > kNone ? __builtin_nanf("") : 0.0f) : 1.0f / total;
 }
 
 // Values rounded to the output type, two to a word.

@@ -44,7 +44,7 @@ template <int D>
 constexpr int kPromptOccupancy = D > 128 ? 1 : 2;
 
 // A run of 16 tokens of a tile: its key scale, log2 and reciprocal of its value
-// scale (the latter in the unit of the sum of weights).
+// scale.
 struct alignas(16) Run {
   float key, lv, iv;
 };
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     auto put_runs = [&](Tile16<D>& to) {
       if (tid < 4) {
         const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
-        to.run[tid] = Run{scale2.x, __log2f(vs), kSumUnit * __builtin_amdgcn_rcpf(vs)};
+        to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs)};
       }
       const uint32_t held = static_cast<uint32_t>(__ballot(held_next)) & 15u;  // lanes 0 .. 3 of wave 0: the four runs
       if (tid == 0) to.held = held;

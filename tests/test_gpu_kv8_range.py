@@ -5,7 +5,7 @@ import pytest
 
 from quantized_linear_layers_packed_amd import qlin
 from tests.gpu_util import say, torch_cuda, workspace
-from tests.test_gpu_kv8 import Setup, back, run_attention, to16
+from tests.test_gpu_kv8 import Setup, back, run_append, run_attention, to16
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,55 @@ def test_scales_of_hidden_pages_may_be_anything(new, window, garbage):
         s.scales[s.table[0, 12:(kv - new - window) // P]] = garbage
     s.upload()
     assert np.isfinite(clean).all() and np.array_equal(back(run_attention(s, 4, F16, window=window, Q=Q)[0]), clean)
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("low,high", [(-80, -76), (-80, -60), (0, 20)])
+def test_value_scales_down_to_the_least_that_append_keeps(call, low, high):
+    D, G, seqs = CALLS[call]
+    say(f"kv8 attention, value scales 2^{low} .. 2^{high}: {call}")
+    L, P = 1801, 16
+    r = np.random.default_rng(3)
+    k, v = (r.integers(-127, 128, (L, D)).astype(np.int8) for _ in range(2))
+    s = Shared(D, P, L, seqs, k, v, 0.02, 2.0 ** r.uniform(low, high, -(-L // P)))
+    s.check(r.standard_normal((1, D)) / np.sqrt(D), G, BF16)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("exponent", [-133, -120, -110, -90, -81, -79, -70])
+def test_attention_and_gather_agree_on_tiny_values(new, exponent):
+    """bf16 values that need scales of 2^exponent: append keeps or drops them, and both readers say the same.  Every token
+    has the same value, so any weights give it back; between the two lie the output's rounding and those of the sums."""
+    torch = torch_cuda()
+    say(f"kv8 append, gather, attention, value scales 2^{exponent}: new={new}")
+    s = Setup(32, 64, 16, 1, [new, new], [new, new])
+    x = s.rng.standard_normal((s.T, 6, 64))
+    value = 2.0 ** exponent * 127 * (1 + np.arange(64) % 8) / 8
+    x[:, 5] = value
+    run_append(s, 4, BF16, 0, False, x=x)
+    s.check_cache()
+    K, V = (torch.empty((s.T, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qlin.qlin_kv8_gather(s.cache, s.batch, K, V, BF16)
+    V = back(V).astype(np.float64)
+    if exponent < -80:
+        assert not V.any() and not s.scales[s.table[s.table >= 0], :, 1].any()
+    else:
+        assert (np.abs(V - value) <= 2.0 ** exponent / 2 * (1 + 2.0 ** -7) + 2.0 ** -8 * value).all()   # a code's, bf16's
+    Y = back(run_attention(s, 4, BF16)[0])
+    assert (np.abs(Y - V) <= (2 * 2.0 ** -8 + 2.0 ** -11 + 200 * 2.0 ** -24) * np.abs(V)).all()
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_tokens_without_values_keep_their_weight_beside_large_values(call):
+    """131 thousand tokens of all-zero values (scale 0) and 2^-18.5 of the weight of a few whose page's scale is 2^15."""
+    D, G, seqs = CALLS[call]
+    say(f"kv8 attention, values of zero beside large ones: {call}")
+    L, P = 131072, 64
+    large = np.zeros(1) if call.startswith("many") else np.arange(0, 512, 64)
+    codes = np.zeros(L, np.int64)
+    codes[large.astype(int)] = 127
+    k, q = by_first_dimension(D, codes)
+    v = np.where(codes[:, None] > 0, np.ones(D, np.int64), 0).astype(np.int8)
+    scales = np.where(v.reshape(-1, P * D).any(axis=1), 2.0 ** 15, 0.0)
+    s = Shared(D, P, L, seqs, k, v, 1.0 / 127, scales)
+    s.check(q(18.5 / LOG2E), G, F16)
