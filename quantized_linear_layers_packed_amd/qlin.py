@@ -394,6 +394,20 @@ class _KvBatch(C.Structure):
                 ("seqs", _i), ("tokens", _i), ("table_stride", _i), ("max_new", _i), ("max_kv", _i)]
 
 
+def _typed(name, t, types):
+    """Refuses a tensor that is of none of the types."""
+    if t.dtype not in types:
+        raise ValueError(f"{name}: {' or '.join(map(str, types))} expected, got {t.dtype}")
+
+
+# What the tensors may hold: codes (or a pool of bytes), indices, and 16-bit values by the call's dtype (16-bit integers
+# are taken as their bits; another dtype is the library's to refuse).
+if torch is not None:
+    _CODES, _INDICES, _F32 = (torch.int8, torch.uint8), (torch.int32, torch.uint32), (torch.float32,)
+    _HALF = {QLIN_F16: (torch.float16, torch.int16, torch.uint16), QLIN_BF16: (torch.bfloat16, torch.int16, torch.uint16)}
+    _ANY = (torch.float16, torch.bfloat16, torch.int16, torch.uint16)
+
+
 class Kv8Cache:
     """A qlin_kv8_cache over three tensors: k_codes int8 [pages][kv_heads][page_size][head_dim], v_codes int8
     [pages][kv_heads][head_dim][page_size], scales fp32 [pages][kv_heads][2].  Keeps them alive; make it once."""
@@ -403,9 +417,9 @@ class Kv8Cache:
         if tuple(v_codes.shape) != (pages, heads, dim, page) or tuple(scales.shape) != (pages, heads, 2):
             raise ValueError(f"v_codes {tuple(v_codes.shape)} and scales {tuple(scales.shape)} do not fit "
                              f"k_codes {tuple(k_codes.shape)}")
-        for name, t, size in (("k_codes", k_codes, 1), ("v_codes", v_codes, 1), ("scales", scales, 4)):
-            if t.element_size() != size:
-                raise ValueError(f"{name}: {size}-byte values expected")
+        _typed("k_codes", k_codes, _CODES)
+        _typed("v_codes", v_codes, _CODES)
+        _typed("scales", scales, _F32)
         self.tensors = (k_codes, v_codes, scales)
         self._c = _KvCache(_ptr(k_codes), _ptr(v_codes), _ptr(scales), pages, heads, dim, page)
         self.ref = C.addressof(self._c)
@@ -422,38 +436,35 @@ class Kv8Batch:
             raise ValueError(f"offsets {tuple(offsets.shape)} and kv_lens {tuple(kv_lens.shape)} do not fit "
                              f"block_table {tuple(block_table.shape)}")
         for name, t in (("offsets", offsets), ("kv_lens", kv_lens), ("block_table", block_table)):
-            if t.element_size() != 4:
-                raise ValueError(f"{name}: int32 expected")
+            _typed(name, t, _INDICES)
         self.tensors = (offsets, kv_lens, block_table)
         self._c = _KvBatch(_ptr(offsets), _ptr(kv_lens), _ptr(block_table), seqs, tokens, stride, max_new, max_kv)
         self.ref = C.addressof(self._c)
         self.tokens = tokens
 
 
-def _rows(x, tokens, heads, dim):
-    """(pointer, token stride in elements) of x [tokens][heads][dim], 16-bit, whose tokens may lie apart."""
+def _rows(x, tokens, heads, dim, types):
+    """(pointer, token stride in elements) of x [tokens][heads][dim], of one of the types, whose tokens may lie apart."""
     if x is None:
         return None, 0
     shape, stride = tuple(x.shape), x.stride()
-    if (shape != (tokens, heads, dim) or x.element_size() != 2 or stride[2] != 1
+    if (shape != (tokens, heads, dim) or x.dtype not in types or stride[2] != 1
             or (heads > 1 and stride[1] != dim)):
-        raise ValueError(f"16-bit [{tokens}][{heads}][{dim}] with contiguous heads expected, got shape {shape}, "
-                         f"strides {tuple(stride)}, {x.element_size()}-byte values")
+        raise ValueError(f"{types[0]} [{tokens}][{heads}][{dim}] with contiguous heads expected, got shape {shape}, "
+                         f"strides {tuple(stride)}, {x.dtype}")
     return x.data_ptr(), stride[0] if tokens > 1 else heads * dim
 
 
-def _out(x, tokens, heads, dim):
-    """Pointer of a contiguous 16-bit tensor of tokens * heads * dim values."""
-    if x is not None and (x.numel() != tokens * heads * dim or x.element_size() != 2):
-        raise ValueError(f"{tokens} * {heads} * {dim} 16-bit values expected, got shape {tuple(x.shape)}, "
-                         f"{x.element_size()}-byte values")
+def _out(x, tokens, heads, dim, types):
+    """Pointer of a contiguous tensor of tokens * heads * dim values of one of the types."""
+    if x is not None and (x.numel() != tokens * heads * dim or x.dtype not in types):
+        raise ValueError(f"{tokens} * {heads} * {dim} values, {types[0]}, expected, got shape {tuple(x.shape)}, {x.dtype}")
     return _ptr(x)
 
 
 def _table(x, rot_dim):
-    if x is not None and (len(x.shape) != 2 or x.shape[1] != rot_dim // 2 or x.element_size() != 4):
-        raise ValueError(f"fp32 [max_pos][{rot_dim // 2}] expected, got shape {tuple(x.shape)}, "
-                         f"{x.element_size()}-byte values")
+    if x is not None and (len(x.shape) != 2 or x.shape[1] != rot_dim // 2 or x.dtype not in _F32):
+        raise ValueError(f"torch.float32 [max_pos][{rot_dim // 2}] expected, got shape {tuple(x.shape)}, {x.dtype}")
     return _ptr(x)
 
 
@@ -467,18 +478,20 @@ def qlin_kv8_append(cache, batch, Q, K, V, dtype, q_heads, cos, sin, rot_dim, ro
     """Q, K, V: tensors [tokens][heads][head_dim], slices of a fused projection's output among them (Q and Q_out may
     be None); cos, sin: fp32 [max_pos][rot_dim / 2] (None without rotation)."""
     T, H, D = batch.tokens, cache.kv_heads, cache.head_dim
-    q, q_stride = _rows(Q, T, q_heads, D)
-    k, k_stride = _rows(K, T, H, D)
-    v, v_stride = _rows(V, T, H, D)
+    half = _HALF.get(dtype, _ANY)
+    q, q_stride = _rows(Q, T, q_heads, D, half)
+    k, k_stride = _rows(K, T, H, D, half)
+    v, v_stride = _rows(V, T, H, D, half)
     max_pos = 0 if cos is None or sin is None else min(cos.shape[0], sin.shape[0])
     _check(_lib.qlin_kv8_append(cache.ref, batch.ref, q, k, v, dtype, q_heads, q_stride, k_stride, v_stride,
                                 _table(cos, rot_dim), _table(sin, rot_dim), max_pos, rot_dim, rope_style,
-                                _out(Q_out, T, q_heads, D), _stream(stream)))
+                                _out(Q_out, T, q_heads, D, half), _stream(stream)))
 
 
 def qlin_kv8_gather(cache, batch, K_out, V_out, dtype, stream=None):
     T, H, D = batch.tokens, cache.kv_heads, cache.head_dim
-    _check(_lib.qlin_kv8_gather(cache.ref, batch.ref, _out(K_out, T, H, D), _out(V_out, T, H, D), dtype,
+    half = _HALF.get(dtype, _ANY)
+    _check(_lib.qlin_kv8_gather(cache.ref, batch.ref, _out(K_out, T, H, D, half), _out(V_out, T, H, D, half), dtype,
                                 _stream(stream)))
 
 
@@ -492,9 +505,10 @@ def qlin_kv8_attention(cache, batch, Q, dtype, q_heads, scale, window, sinks, Y,
                        stream=None):
     """Q: a tensor [tokens][q_heads][head_dim], slices of a fused projection's output among them."""
     T, D = batch.tokens, cache.head_dim
-    q, q_stride = _rows(Q, T, q_heads, D)
+    half = _HALF.get(dtype, _ANY)
+    q, q_stride = _rows(Q, T, q_heads, D, half)
     _check(_lib.qlin_kv8_attention(cache.ref, batch.ref, q, dtype, q_heads, q_stride, scale, window, sinks,
-                                   _out(Y, T, q_heads, D), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                   _out(Y, T, q_heads, D, half), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                    _stream(stream)))
 
 
