@@ -342,7 +342,8 @@ qlin_status qlin_f16_gemm(const uint16_t* X, const uint16_t* W, int M, int N, in
  * (with codes of 0) or at least 2^-80, as append keeps them.  Beside values with
  * scales above 2^20, tokens of scales 2^100 times smaller may lose their weight.
  * head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; num_pages * kv_heads
- * below 2^31 (EUNSUPPORTED otherwise).  Offsets into the pool are 64-bit.     */
+ * below 2^31, kv_heads <= 32767 (EUNSUPPORTED otherwise).  Offsets into the pool
+ * are 64-bit. */
 typedef struct {
   int8_t* k_codes;
   int8_t* v_codes;
@@ -399,7 +400,8 @@ qlin_status qlin_kv8_sizes(int num_pages, int kv_heads, int head_dim, int page_s
  * is started anew): whoever sees a token of it gets NaN, nobody else does.
  * No two sequences of a call may store into the same page.  Requirements: seqs,
  * tokens, q_heads, max_new, max_kv > 0, q_heads a multiple of kv_heads (ignored
- * without Q), tokens * heads * head_dim < 2^40, seqs and heads <= 65535. */
+ * without Q), tokens * stride <= 2^40 for each of the strides, seqs and q_heads <=
+ * 65535. */
 qlin_status qlin_kv8_append(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
                             const void* Q, const void* K, const void* V, int dtype, int q_heads,
                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -408,7 +410,8 @@ qlin_status qlin_kv8_append(const qlin_kv8_cache* cache, const qlin_kv8_batch* b
 
 /* The cached values of the batch's tokens (keys as rotated) back in 16 bits:
  * K_out, V_out device [tokens][kv_heads][head_dim] of dtype QLIN_F16 or QLIN_BF16,
- * scale * code rounded once (0 for tokens that are not stored). */
+ * scale * code rounded to it, for BF16 by way of fp32 (0 for tokens that are not
+ * stored). */
 qlin_status qlin_kv8_gather(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
                             void* K_out, void* V_out, int dtype, hipStream_t stream);
 
@@ -433,7 +436,8 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
  * holds 16 or 32 rows and splits the cache over its waves up to 64 rows (with
  * head_dim 256 up to 16, or 32 where seqs * kv_heads >= 8); otherwise one that
  * holds 128 or 256 rows and shares tiles of the cache; in batches of eight and
- * more sequences each takes those that suit it.
+ * more sequences each takes those that suit it.  Fewer sequences that mix a
+ * prompt with single tokens over long caches are faster as two calls.
  * Codes enter the matrix instructions as exact fp16 integers and products are
  * summed in fp32; bf16 queries are scaled to fp16 by a power of two per row (as
  * in qlin_w4_forward); softmax statistics are fp32; the weights are rounded to

@@ -17,7 +17,7 @@ namespace qlin {
 // any will do that keeps the weights of such a page, 2^(score - reference) times the
 // scale, and their sum without the scale in fp32's range: it is below 2^(15 + 80 +
 // 31) for any number of tokens, and beside values with scales of up to 2^20 weights
-// of 2^-33 of the row's largest still count.
+// of 2^-26 of the row's largest still count, also where splits are joined.
 constexpr float kLeastScale = 8.2718061e-25f;
 
 // Cache and batch with the sizes that the host has checked.

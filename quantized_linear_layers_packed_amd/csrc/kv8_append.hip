@@ -24,7 +24,7 @@
 //
 // Measured: ragged prompts of 8.8 thousand tokens, 64 / 8 heads of 128, pages of 32:
 // 84 us for 337 MB, 4.0 TB/s (a large copy: 4.8), of which the queries' part is 70;
-// reading the touched pages back 15 us.  One token of one sequence: 5.6 and 4.7 us, a
+// reading the touched pages back 15 us.  One token of one sequence: 5.6 and 4.8 us, a
 // chain of launch, lengths, page number, scale and store.  Tried without gain:
 // queries read past the caches (+5 %), written past them (faster for long pages,
 // 22 % slower here), the page's scale and boundary piece fetched before the new

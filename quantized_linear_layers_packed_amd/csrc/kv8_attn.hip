@@ -430,7 +430,7 @@ size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
   // compute unit, also where two would fit: twice the splits cost more than they
   // hide (131072 tokens 50 -> 59 us).  Row tiles of a prompt differ in length and
   // are not split once there is one for every workgroup that fits.  Up to 256 splits
-  // for many rows (32 rows of 8 heads over 131072 tokens 70 us with 64, 39 with 256).
+  // for many rows (256 rows of one head over 131072 tokens 70 us with 64, 39 with 256).
   const long long slots = static_cast<long long>(cus) * (nt ? 1 : kv8_prompt_resident(a->c.dim));
   const long long steps = nt ? a->waves : 1, alone = 3, split = 5;
   const long long most_splits = nt ? kMostSplits : kMostManySplits;

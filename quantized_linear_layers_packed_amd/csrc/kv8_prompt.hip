@@ -14,7 +14,7 @@
 // A run of 16 tokens lies in one page: its two scales are the same for every lane.
 //
 // Bound by the matrix and vector units together, under the power limit: a prompt
-// of 8192 with 64 / 8 heads of 128 runs at 0.95 PFLOP/s (a large fp16 product of
+// of 8192 with 64 / 8 heads of 128 runs at 0.96 PFLOP/s (a large fp16 product of
 // the library at 1.17), 1.1 on operands of zeros; the matrix units are busy 45 %
 // of the cycles, the vector units (an exponential, a multiply-add, a sum, half a
 // maximum and half a conversion for each score) about 55 %.  Taking the
@@ -62,7 +62,7 @@ struct alignas(16) Tile16 {
 // Schedules the N products of this block, whose A operands come from LDS, so that a
 // product's operand is on its way six products ahead, and ends the scheduling
 // region.  The compiler alone asks for it one product ahead and waits each time:
-// heads of 256, one wave to a SIMD: 4096 rows of 16 heads 230 -> 202 us; heads of
+// heads of 256, one wave to a SIMD: a prompt of 4096 with 16 heads 230 -> 202 us; heads of
 // 128: 1046 -> 1001 us on operands of zeros, where the clock does not sink.
 template <int N>
 __device__ __forceinline__ void lookahead() {
