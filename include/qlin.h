@@ -450,6 +450,76 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ======================================================================== */
+/* Pages of the 8-bit cache: who holds which, forks, compaction, copies      */
+/* ======================================================================== */
+/* A book on the device says which pages of a pool are in use: refs[p] is the
+ * number of block table entries that hold page p (0: free).  Rows of its table
+ * are sequences (a qlin_kv8_batch may use the same table), entries outside
+ * 0 .. num_pages-1 hold nothing; the calls write -1 there.  A new book has zeros
+ * and -1 everywhere.  Any number of caches (the layers of a model) may share a book;
+ * the calls below change the book alone and say in `moves` which pages are to be
+ * copied in each of them, which qlin_kv8_copy_pages then does.
+ * Choices depend on the book alone: free pages are taken from the lowest on, in
+ * the order of rows (forks) and entries, so a replayed graph repeats them exactly.
+ * A call that cannot do all of its work changes nothing in the book.  Calls on one
+ * book must not overlap in time.
+ *   moves device int32 [1 + n][2]: first (count, short), then `count` pairs of
+ *     pages (from, to), -1, -1 for none.  short: 0, the number of free pages that
+ *     were missing, or -1 for lists or lengths that do not fit the table (count is 0
+ *     then)
+ * Requirements: page_size 16, 32, 64 or 128, num_pages <= 2^30, rows <= 32767,
+ * rows * table_stride < 2^31 (EUNSUPPORTED). */
+typedef struct {
+  int32_t* refs;               /* device [num_pages] */
+  int32_t* block_table;        /* device [rows][table_stride] */
+  int num_pages, page_size, rows, table_stride;
+} qlin_kv8_book;
+
+/* Pages for longer sequences: in each row b, the entries behind its last held one
+ * below ceil(lens[b] / page_size), up to that one, get a page each (entries before
+ * it, given back behind a sliding window, stay empty).  lens device int32 [rows];
+ * rows of lengths up to 0 get nothing, a length past the table's end is refused
+ * (short -1).  moves int32 [1][2]: the pages taken, and short. */
+qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_t* moves, hipStream_t stream);
+
+/* Sequences that go on from the first lens[i] tokens of another: row children[i]
+ * shares the full pages of row parents[i] and, where the prefix ends inside a
+ * page, gets a fresh one, moves[1 + i] = (the parent's page, it), to be copied before
+ * either sequence is appended to.  Entries behind are -1; pages that the child's
+ * row held are given back (they serve later calls).
+ * Lists: device int32 [count], count <= 16384; a negative parent or child marks an
+ * entry of padding.  Refused (short -1, nothing done): rows past the table, lengths
+ * below 0 or past the table, a child named twice or as a parent.
+ * A sequence that is cut back into a page that it shares must not be appended to:
+ * fork its prefix to another row instead.  moves int32 [1 + count][2]. */
+qlin_status qlin_kv8_fork(const qlin_kv8_book* book, const int32_t* parents, const int32_t* children, const int32_t* lens,
+                          int count, int32_t* moves, hipStream_t stream);
+
+/* Gives back the entries of rows[i] whose tokens all lie in positions begin[i] ..
+ * end[i]-1 (NULL: from 0 on, to the table's end): whole sequences, pages behind a
+ * window, pages of rejected drafts.  A page is free once nothing holds it.  Rows
+ * outside the table are skipped, rows may be named more than once.  Lists: device
+ * int32 [count], count <= 65535. */
+qlin_status qlin_kv8_free(const qlin_kv8_book* book, const int32_t* rows, const int32_t* begin, const int32_t* end,
+                          int count, hipStream_t stream);
+
+/* Moves pages in use to the front of the pool: the i-th lowest free page takes the
+ * place of the i-th highest used one while that lies above it, at most `most` of them
+ * (no more than num_pages / 2 are ever needed).  Table and refs follow; pages that
+ * refs counts but no entry holds move too.  moves int32 [1 + most][2], all written:
+ * copy them before the moved pages are read. */
+qlin_status qlin_kv8_compact(const qlin_kv8_book* book, int most, int32_t* moves, hipStream_t stream);
+
+/* Copies codes and scales of the pages listed in moves (as above, at most `most`
+ * pairs), from from[l] to to[l] for each of `layers` caches (host arrays of
+ * descriptors; all of the same kv_heads, head_dim and page_size, those of one side of
+ * the same num_pages).  Both sides may be the same caches; pages are copied in no
+ * order, so none may be written twice, or written and read.  Pairs with a page
+ * outside its pool are skipped.  Pages up to 4 GiB (EUNSUPPORTED). */
+qlin_status qlin_kv8_copy_pages(const qlin_kv8_cache* to, const qlin_kv8_cache* from, int layers, const int32_t* moves,
+                                int most, hipStream_t stream);
+
+/* ======================================================================== */
 /* Second-order encoders (host, offline): same storage, same forward calls   */
 /* ======================================================================== */
 /* The GPTQ bulletin ("İddia ve Gerçeklik") quantizes column by column with a

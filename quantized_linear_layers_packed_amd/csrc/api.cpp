@@ -258,6 +258,33 @@ qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qli
   return QLIN_OK;
 }
 
+// A book of pages as the kernels see it.
+qlin_status kv8_book(const char* fn, const qlin_kv8_book* b, Kv8Book* k) {
+  if (!b) return fail(QLIN_EINVAL, std::string(fn) + ": NULL book");
+  if (b->num_pages <= 0 || b->page_size <= 0 || b->rows <= 0 || b->table_stride <= 0)
+    return fail(QLIN_EINVAL, std::string(fn) + ": num_pages, page_size, rows and table_stride must be positive");
+  if (b->page_size != 16 && b->page_size != 32 && b->page_size != 64 && b->page_size != 128)
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": page_size must be 16, 32, 64 or 128");
+  if (b->num_pages > (1 << 30)) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": num_pages above 2^30");
+  if (b->rows > kMostRows)
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": rows above " + std::to_string(kMostRows));
+  if (static_cast<int64_t>(b->rows) * b->table_stride > INT32_MAX)
+    return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": rows * table_stride must be below 2^31");
+  if (!b->refs || !b->block_table) return fail(QLIN_EINVAL, std::string(fn) + ": NULL refs or block_table");
+  QLIN_TRY(need_aligned(fn, "refs", b->refs));
+  QLIN_TRY(need_aligned(fn, "block_table", b->block_table));
+  int log_page = 4;
+  while ((1 << log_page) < b->page_size) ++log_page;
+  *k = Kv8Book{b->refs, b->block_table, b->num_pages, log_page, b->rows, b->table_stride};
+  return QLIN_OK;
+}
+
+// A list of int32 on the device.
+qlin_status kv8_list(const char* fn, const char* name, const void* p) {
+  if (!p) return fail(QLIN_EINVAL, std::string(fn) + ": NULL " + name);
+  return need_aligned(fn, name, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -567,6 +594,99 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
   QLIN_TRY(need_workspace(fn, workspace, workspace_bytes, total));
   const WsView ws{static_cast<char*>(workspace), workspace_bytes};
   kv8_attn_launch(plan, total ? ws.counters() : nullptr, total ? static_cast<char*>(ws.partials()) : nullptr, dtype, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_t* moves, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_grow";
+  clear_error();
+  Kv8Book k;
+  QLIN_TRY(kv8_book(fn, book, &k));
+  QLIN_TRY(kv8_list(fn, "lens", lens));
+  QLIN_TRY(kv8_list(fn, "moves", moves));
+  kv8_grow_launch(k, lens, moves, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_fork(const qlin_kv8_book* book, const int32_t* parents, const int32_t* children, const int32_t* lens,
+                          int count, int32_t* moves, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_fork";
+  clear_error();
+  Kv8Book k;
+  QLIN_TRY(kv8_book(fn, book, &k));
+  if (count <= 0) return fail(QLIN_EINVAL, std::string(fn) + ": count must be positive");
+  if (count > kMostForks) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": count above " + std::to_string(kMostForks));
+  QLIN_TRY(kv8_list(fn, "parents", parents));
+  QLIN_TRY(kv8_list(fn, "children", children));
+  QLIN_TRY(kv8_list(fn, "lens", lens));
+  QLIN_TRY(kv8_list(fn, "moves", moves));
+  kv8_fork_launch(k, parents, children, lens, count, moves, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_free(const qlin_kv8_book* book, const int32_t* rows, const int32_t* begin, const int32_t* end,
+                          int count, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_free";
+  clear_error();
+  Kv8Book k;
+  QLIN_TRY(kv8_book(fn, book, &k));
+  if (count <= 0) return fail(QLIN_EINVAL, std::string(fn) + ": count must be positive");
+  if (count > 65535) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": count above 65535");
+  QLIN_TRY(kv8_list(fn, "rows", rows));
+  if (begin) QLIN_TRY(need_aligned(fn, "begin", begin));
+  if (end) QLIN_TRY(need_aligned(fn, "end", end));
+  kv8_free_launch(k, rows, begin, end, count, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_compact(const qlin_kv8_book* book, int most, int32_t* moves, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_compact";
+  clear_error();
+  Kv8Book k;
+  QLIN_TRY(kv8_book(fn, book, &k));
+  if (most <= 0) return fail(QLIN_EINVAL, std::string(fn) + ": most must be positive");
+  QLIN_TRY(kv8_list(fn, "moves", moves));
+  kv8_compact_launch(k, most, moves, stream);
+  return check_launch(fn);
+}
+
+qlin_status qlin_kv8_copy_pages(const qlin_kv8_cache* to, const qlin_kv8_cache* from, int layers, const int32_t* moves,
+                                int most, hipStream_t stream) {
+  static const char* fn = "qlin_kv8_copy_pages";
+  clear_error();
+  if (!to || !from) return fail(QLIN_EINVAL, std::string(fn) + ": NULL to or from");
+  if (layers <= 0 || most <= 0) return fail(QLIN_EINVAL, std::string(fn) + ": layers and most must be positive");
+  for (int i = 0; i < layers; ++i)
+    for (const qlin_kv8_cache* c : {to + i, from + i}) {
+      QLIN_TRY(kv8_check_sizes(fn, c->num_pages, c->kv_heads, c->head_dim, c->page_size));
+      if (c->kv_heads != to->kv_heads || c->head_dim != to->head_dim || c->page_size != to->page_size)
+        return fail(QLIN_EINVAL, std::string(fn) + ": caches of different kv_heads, head_dim or page_size");
+      if (c->num_pages != (c == to + i ? to : from)->num_pages)
+        return fail(QLIN_EINVAL, std::string(fn) + ": layers of different num_pages");
+      if (!c->k_codes || !c->v_codes || !c->scales) return fail(QLIN_EINVAL, std::string(fn) + ": NULL cache pointer");
+      QLIN_TRY(need_aligned(fn, "k_codes", c->k_codes));
+      QLIN_TRY(need_aligned(fn, "v_codes", c->v_codes));
+      QLIN_TRY(need_aligned(fn, "scales", c->scales));
+    }
+  const int64_t chunks = static_cast<int64_t>(to->kv_heads) * to->head_dim * to->page_size / 16;
+  if (chunks > (1 << 28)) return fail(QLIN_EUNSUPPORTED, std::string(fn) + ": pages above 4 GiB");
+  QLIN_TRY(kv8_list(fn, "moves", moves));
+  Kv8CopyArgs a{};
+  a.moves = reinterpret_cast<const int2*>(moves);
+  a.most = most;
+  a.chunks = static_cast<int>(chunks);
+  a.heads = to->kv_heads;
+  a.from_pages = from->num_pages;
+  a.to_pages = to->num_pages;
+  for (int at = 0; at < layers; at += kCopyLayers) {
+    const int n = std::min(layers - at, kCopyLayers);
+    for (int i = 0; i < n; ++i) {
+      const qlin_kv8_cache &f = from[at + i], &t = to[at + i];
+      a.layers[i] = Kv8CopyLayer{f.k_codes, f.v_codes, reinterpret_cast<const float2*>(f.scales),
+                                 t.k_codes, t.v_codes, reinterpret_cast<float2*>(t.scales)};
+    }
+    kv8_copy_launch(a, n, stream);
+  }
   return check_launch(fn);
 }
 

@@ -96,6 +96,39 @@ struct Kv8AttnArgs {
   float* partials;
 };
 
+// The book of a cache's pages with the sizes that the host has checked.
+struct Kv8Book {
+  int32_t* refs;
+  int32_t* table;
+  int pages, log_page, rows, stride;
+};
+
+// Copies of listed pages, layer by layer.
+constexpr int kCopyLayers = 32;           // of a launch
+struct Kv8CopyLayer {
+  const int8_t* from_k;
+  const int8_t* from_v;
+  const float2* from_scales;
+  int8_t* to_k;
+  int8_t* to_v;
+  float2* to_scales;
+};
+struct Kv8CopyArgs {
+  const int2* moves;
+  int most, chunks, heads, from_pages, to_pages;   // chunks: 16-byte ones of a page's K
+  Kv8CopyLayer layers[kCopyLayers];
+};
+
+constexpr int kMostRows = 32767;          // of a book: a workgroup holds an integer for each
+constexpr int kMostForks = 16384;
+
+void kv8_grow_launch(const Kv8Book& k, const int32_t* lens, int32_t* moves, hipStream_t stream);
+void kv8_fork_launch(const Kv8Book& k, const int32_t* parents, const int32_t* children, const int32_t* lens, int n,
+                     int32_t* moves, hipStream_t stream);
+void kv8_free_launch(const Kv8Book& k, const int32_t* rows, const int32_t* begin, const int32_t* end, int n, hipStream_t stream);
+void kv8_compact_launch(const Kv8Book& k, int most, int32_t* moves, hipStream_t stream);
+void kv8_copy_launch(Kv8CopyArgs a, int layers, hipStream_t stream);
+
 void kv8_append_launch(const Kv8AppendArgs& a, int dtype, hipStream_t stream);
 void kv8_gather_launch(const Kv8View& c, uint16_t* K, uint16_t* V, int dtype, hipStream_t stream);
 

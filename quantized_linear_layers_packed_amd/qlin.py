@@ -50,6 +50,7 @@ EXPORTS = (
     "qlin_w4_workspace_bytes", "sq_int8_gemm_workspace_bytes", "qlin_w4_forward_scratch",
     "qlin_mfma_peak", "spqr_workspace_bytes", "qlin_f16_gemm", "qlin_f16_gemm_workspace_bytes",
     "qlin_kv8_sizes", "qlin_kv8_append", "qlin_kv8_gather", "qlin_kv8_attention", "qlin_kv8_attention_workspace_bytes",
+    "qlin_kv8_grow", "qlin_kv8_fork", "qlin_kv8_free", "qlin_kv8_compact", "qlin_kv8_copy_pages",
 )
 
 _vp, _i, _i64, _sz, _d, _f = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_double, C.c_float
@@ -89,6 +90,11 @@ _sigs = {
     "qlin_kv8_gather": ([_vp, _vp, _vp, _vp, _i, _vp], _i),
     "qlin_kv8_attention": ([_vp, _vp, _vp, _i, _i, _i64, _f, _i, _i, _vp, _vp, _sz, _vp], _i),
     "qlin_kv8_attention_workspace_bytes": ([_vp, _vp, _i, _i, _i, _vp], _i),
+    "qlin_kv8_grow": ([_vp, _vp, _vp, _vp], _i),
+    "qlin_kv8_fork": ([_vp, _vp, _vp, _vp, _i, _vp, _vp], _i),
+    "qlin_kv8_free": ([_vp, _vp, _vp, _vp, _i, _vp], _i),
+    "qlin_kv8_compact": ([_vp, _i, _vp, _vp], _i),
+    "qlin_kv8_copy_pages": ([_vp, _vp, _i, _vp, _i, _vp], _i),
 }
 for _name, (_args, _res) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -510,6 +516,90 @@ def qlin_kv8_attention(cache, batch, Q, dtype, q_heads, scale, window, sinks, Y,
     _check(_lib.qlin_kv8_attention(cache.ref, batch.ref, q, dtype, q_heads, q_stride, scale, window, sinks,
                                    _out(Y, T, q_heads, D, half), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                    _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Pages of the 8-bit cache
+
+class _KvBook(C.Structure):
+    _fields_ = [("refs", _vp), ("block_table", _vp), ("num_pages", _i), ("page_size", _i), ("rows", _i), ("table_stride", _i)]
+
+
+class Kv8Book:
+    """A qlin_kv8_book over two int32 tensors: refs [num_pages] (zeros in a new book) and block_table [rows][table_stride]
+    (-1 in a new book).  Keeps them alive."""
+
+    def __init__(self, refs, block_table, page_size):
+        if len(refs.shape) != 1 or len(block_table.shape) != 2:
+            raise ValueError(f"refs [num_pages] and block_table [rows][table_stride] expected, got shapes {tuple(refs.shape)}, "
+                             f"{tuple(block_table.shape)}")
+        _typed("refs", refs, _INDICES)
+        _typed("block_table", block_table, _INDICES)
+        self.tensors = (refs, block_table)
+        self.rows, stride = block_table.shape
+        self._c = _KvBook(_ptr(refs), _ptr(block_table), refs.shape[0], page_size, self.rows, stride)
+        self.ref = C.addressof(self._c)
+
+
+class Kv8Caches:
+    """The caches of several layers, for calls that take them all.  Keeps them alive; make it once."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        self.count = len(self.caches)
+        self._c = (_KvCache * self.count)(*(c._c for c in self.caches))
+        self.ref = C.addressof(self._c)
+
+
+def _list(name, t, count):
+    """Pointer of an int32 tensor [count]."""
+    if tuple(t.shape) != (count,):
+        raise ValueError(f"{name}: [{count}] expected, got shape {tuple(t.shape)}")
+    _typed(name, t, _INDICES)
+    return _ptr(t)
+
+
+def _moves(t, least=0):
+    """(pointer, pairs after the first) of moves int32 [1 + n][2], n at least `least`."""
+    if len(t.shape) != 2 or t.shape[1] != 2 or t.shape[0] < 1 + least:
+        raise ValueError(f"moves: [{1 + least} or more][2] expected, got shape {tuple(t.shape)}")
+    _typed("moves", t, _INDICES)
+    return _ptr(t), t.shape[0] - 1
+
+
+def qlin_kv8_grow(book, lens, moves, stream=None):
+    """lens int32 [rows]; moves int32 [1][2] (or longer, of which the first pair is written)."""
+    _check(_lib.qlin_kv8_grow(book.ref, _list("lens", lens, book.rows), _moves(moves)[0], _stream(stream)))
+
+
+def qlin_kv8_fork(book, parents, children, lens, moves, stream=None):
+    """parents, children, lens int32 [count]; moves int32 [1 + count][2] (or longer)."""
+    n = parents.shape[0]
+    _check(_lib.qlin_kv8_fork(book.ref, _list("parents", parents, n), _list("children", children, n), _list("lens", lens, n),
+                              n, _moves(moves, n)[0], _stream(stream)))
+
+
+def qlin_kv8_free(book, rows, begin=None, end=None, stream=None):
+    """rows, begin, end int32 [count]; without begin and end whole rows."""
+    n = rows.shape[0]
+    _check(_lib.qlin_kv8_free(book.ref, _list("rows", rows, n), None if begin is None else _list("begin", begin, n),
+                              None if end is None else _list("end", end, n), n, _stream(stream)))
+
+
+def qlin_kv8_compact(book, moves, stream=None):
+    """moves int32 [1 + most][2]."""
+    p, most = _moves(moves, 1)
+    _check(_lib.qlin_kv8_compact(book.ref, most, p, _stream(stream)))
+
+
+def qlin_kv8_copy_pages(to, source, moves, stream=None):
+    """to, source: a Kv8Cache each, or Kv8Caches of as many layers; moves int32 [1 + n][2], filled by qlin_kv8_fork or
+    qlin_kv8_compact or by the caller."""
+    p, most = _moves(moves, 1)
+    layers = getattr(to, "count", 1)
+    if getattr(source, "count", 1) != layers:
+        raise ValueError(f"{layers} layers to copy to, {getattr(source, 'count', 1)} to copy from")
+    _check(_lib.qlin_kv8_copy_pages(to.ref, source.ref, layers, p, most, _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
