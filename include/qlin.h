@@ -39,7 +39,7 @@
  *     share a workspace.  The library keeps no state besides the thread-local
  *     error message and a per-device cache of the compute-unit count.
  *   - Workspace (qlin_w4_forward, qlin_w4_forward_perm, spqr_forward,
- *     sq_int8_gemm, qlin_f16_gemm, qlin_kv8_attention): device
+ *     sq_int8_gemm, qlin_f16_gemm, qlin_kv8_attention and its _scored form): device
  *     memory of at least the size the matching *_workspace_bytes call reports
  *     for the shape (0 means none is needed and NULL may be passed), 16-byte
  *     aligned.  Fill the whole buffer with zeros once after allocating it:
@@ -448,6 +448,35 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
                                const void* Q, int dtype, int q_heads, int64_t q_stride,
                                float scale, int window, int sinks, void* Y,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Other scores and masks.  With x = scale q.k and the query at position p, in this
+ * order:
+ *   cap > 0        x becomes cap tanh(x / cap); cap from 2^-10 to 2^10, 0: none
+ *   slopes         x -= slopes[query head] * |p - j|; NULL: none
+ *   prefix_lens    positions j < prefix_lens[b] of sequence b are visible to its queries
+ *                  at earlier positions too (a prefix read in both directions; queries
+ *                  behind it see it anyway); NULL: none
+ *   starts         the query of token t sees no position before starts[t] (documents that
+ *                  are packed into one sequence; first tokens that stay visible count
+ *                  from there); NULL: all from 0 on
+ * The query sees j >= start with j <= p or j < prefix, and, for window > 0, with j > p -
+ * window or j < start + sinks.  Prefixes and starts are clamped to the sequence's tokens. */
+typedef struct {
+  float cap;
+  const float* slopes;         /* device [q_heads] */
+  const int32_t* prefix_lens;  /* device [seqs] */
+  const int32_t* starts;       /* device [tokens] */
+} qlin_kv8_scoring;
+
+/* qlin_kv8_attention with these scores and masks; all else, the workspace among it, as
+ * there.  A capped score is within 2^-21 cap of the formula's; infinite ones are cap or
+ * -cap.  2 log2(e) scale / cap has to be finite.  Positions up to 2^24 apart are exact in
+ * the bias, which is added in fp32.  Tiles that no row of a tile of queries sees are not
+ * read: packed documents cost what they see, not the square of their sum. */
+qlin_status qlin_kv8_attention_scored(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
+                                      const void* Q, int dtype, int q_heads, int64_t q_stride,
+                                      float scale, int window, int sinks, const qlin_kv8_scoring* scoring, void* Y,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ======================================================================== */
 /* Pages of the 8-bit cache: who holds which, forks, compaction, copies      */

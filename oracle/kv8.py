@@ -137,3 +137,43 @@ def attention(k_codes, v_codes, scales, offsets, kv_lens, table, Q, scale, windo
                     score[row + i, hq] = (np.abs(ks) @ np.abs(q)).max() * scale
                     peak[row + i, hq] = np.abs(vs).max()
     return Y, A, score, peak
+
+
+def attention_scored(k_codes, v_codes, scales, offsets, kv_lens, table, Q, scale, window, sinks, cap=0.0, slopes=None,
+                     prefix_lens=None, starts=None):
+    """As attention, with scores capped by cap tanh(x / cap) and lowered by slopes[head] |p - j|, prefixes of sequences
+    that all their queries see, and first visible positions of tokens; also per row the largest visible slope |p - j|."""
+    T, Hq, D = Q.shape
+    Hk = k_codes.shape[1]
+    G = Hq // Hk
+    Y, A = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    score, peak, far = np.zeros((T, Hq)), np.zeros((T, Hq)), np.zeros((T, Hq))
+    for b in range(len(kv_lens)):
+        row, n, m = int(offsets[b]), int(offsets[b + 1] - offsets[b]), int(kv_lens[b])
+        j = np.arange(m)
+        for h in range(Hk):
+            k, v, held = values(k_codes, v_codes, scales, table[b], m, h)
+            for i in range(n):
+                p = m - n + i
+                start = max(int(starts[row + i]), 0) if starts is not None else 0
+                seen = (j <= p) | ((j < int(prefix_lens[b])) if prefix_lens is not None else False)
+                if window:
+                    seen &= (j > p - window) | (j < start + sinks)
+                seen &= held & (j >= start) & (p >= 0)
+                if not seen.any():
+                    continue
+                ks, vs, away = k[seen], v[seen], np.abs(p - j[seen]).astype(np.float64)
+                for hq in range(h * G, h * G + G):
+                    q = Q[row + i, hq].astype(np.float64)
+                    x = (ks @ q) * scale
+                    if cap:
+                        x = cap * np.tanh(x / cap)
+                    if slopes is not None:
+                        x = x - float(slopes[hq]) * away
+                        far[row + i, hq] = abs(float(slopes[hq])) * away.max()
+                    w = np.exp(x - x.max())
+                    w /= w.sum()
+                    Y[row + i, hq], A[row + i, hq] = w @ vs, w @ np.abs(vs)
+                    score[row + i, hq] = (np.abs(ks) @ np.abs(q)).max() * scale
+                    peak[row + i, hq] = np.abs(vs).max()
+    return Y, A, score, peak, far

@@ -258,6 +258,33 @@ qlin_status kv8_attn_args(const char* fn, const qlin_kv8_cache* cache, const qli
   return QLIN_OK;
 }
 
+// The attention calls with their scoring in `a` (the plan copies it).
+qlin_status kv8_attention_checked(const char* fn, Kv8AttnArgs a, const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
+                                  const void* Q, int dtype, int q_heads, int64_t q_stride, float scale, int window, int sinks,
+                                  void* Y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.q_stride = q_stride;
+  a.Y = static_cast<uint16_t*>(Y);
+  Kv8AttnPlan plan;
+  size_t total = 0;
+  QLIN_TRY(kv8_attn_args(fn, cache, batch, q_heads, window, sinks, false, &a, &plan, &total));
+  QLIN_TRY(kv8_check_dtype(fn, dtype));
+  if (!Q || !Y) return fail(QLIN_EINVAL, std::string(fn) + ": NULL Q or Y");
+  if (!(scale > 0.0f) || !std::isfinite(a.scale))
+    return fail(QLIN_EINVAL, std::string(fn) + (a.cap > 0.0f ? ": scale and 2 * log2(e) * scale / cap must be finite and positive"
+                                                            : ": scale and scale * log2(e) must be finite and positive"));
+  QLIN_TRY(need_aligned(fn, "Q", Q));
+  QLIN_TRY(need_aligned(fn, "Y", Y));
+  QLIN_TRY(kv8_check_rows(fn, "q_stride", a.c.tokens, q_heads, a.c.dim, q_stride));
+  if (kv8_overlap(Q, kv8_span(a.c.tokens, q_heads, a.c.dim, q_stride), Y,
+                  kv8_span(a.c.tokens, q_heads, a.c.dim, static_cast<int64_t>(q_heads) * a.c.dim)))
+    return fail(QLIN_EINVAL, std::string(fn) + ": Y overlaps Q");
+  QLIN_TRY(need_workspace(fn, workspace, workspace_bytes, total));
+  const WsView ws{static_cast<char*>(workspace), workspace_bytes};
+  kv8_attn_launch(plan, total ? ws.counters() : nullptr, total ? static_cast<char*>(ws.partials()) : nullptr, dtype, stream);
+  return check_launch(fn);
+}
+
 // A book of pages as the kernels see it.
 qlin_status kv8_book(const char* fn, const qlin_kv8_book* b, Kv8Book* k) {
   if (!b) return fail(QLIN_EINVAL, std::string(fn) + ": NULL book");
@@ -570,31 +597,38 @@ qlin_status qlin_kv8_attention_workspace_bytes(const qlin_kv8_cache* cache, cons
 qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, const void* Q, int dtype,
                                int q_heads, int64_t q_stride, float scale, int window, int sinks, void* Y,
                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  static const char* fn = "qlin_kv8_attention";
   clear_error();
   Kv8AttnArgs a{};
-  // (the plan copies these)
-  a.Q = static_cast<const uint16_t*>(Q);
-  a.q_stride = q_stride;
   a.scale = scale * 1.44269504088896340736f;   // log2(e)
-  a.Y = static_cast<uint16_t*>(Y);
-  Kv8AttnPlan plan;
-  size_t total = 0;
-  QLIN_TRY(kv8_attn_args(fn, cache, batch, q_heads, window, sinks, false, &a, &plan, &total));
-  QLIN_TRY(kv8_check_dtype(fn, dtype));
-  if (!Q || !Y) return fail(QLIN_EINVAL, std::string(fn) + ": NULL Q or Y");
-  if (!(scale > 0.0f) || !std::isfinite(a.scale))
-    return fail(QLIN_EINVAL, std::string(fn) + ": scale and scale * log2(e) must be finite and positive");
-  QLIN_TRY(need_aligned(fn, "Q", Q));
-  QLIN_TRY(need_aligned(fn, "Y", Y));
-  QLIN_TRY(kv8_check_rows(fn, "q_stride", a.c.tokens, q_heads, a.c.dim, q_stride));
-  if (kv8_overlap(Q, kv8_span(a.c.tokens, q_heads, a.c.dim, q_stride), Y,
-                  kv8_span(a.c.tokens, q_heads, a.c.dim, static_cast<int64_t>(q_heads) * a.c.dim)))
-    return fail(QLIN_EINVAL, std::string(fn) + ": Y overlaps Q");
-  QLIN_TRY(need_workspace(fn, workspace, workspace_bytes, total));
-  const WsView ws{static_cast<char*>(workspace), workspace_bytes};
-  kv8_attn_launch(plan, total ? ws.counters() : nullptr, total ? static_cast<char*>(ws.partials()) : nullptr, dtype, stream);
-  return check_launch(fn);
+  return kv8_attention_checked("qlin_kv8_attention", a, cache, batch, Q, dtype, q_heads, q_stride, scale, window, sinks, Y,
+                               workspace, workspace_bytes, stream);
+}
+
+qlin_status qlin_kv8_attention_scored(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch, const void* Q, int dtype,
+                                      int q_heads, int64_t q_stride, float scale, int window, int sinks,
+                                      const qlin_kv8_scoring* scoring, void* Y, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+  static const char* fn = "qlin_kv8_attention_scored";
+  clear_error();
+  if (!scoring) return fail(QLIN_EINVAL, std::string(fn) + ": NULL scoring");
+  const float cap = scoring->cap;
+  if (cap != 0.0f && !(cap >= 0.0009765625f && cap <= 1024.0f))
+    return fail(QLIN_EINVAL, std::string(fn) + ": cap must be 0 or from 2^-10 to 2^10");
+  if (scoring->slopes) QLIN_TRY(need_aligned(fn, "slopes", scoring->slopes));
+  if (scoring->prefix_lens) QLIN_TRY(need_aligned(fn, "prefix_lens", scoring->prefix_lens));
+  if (scoring->starts) QLIN_TRY(need_aligned(fn, "starts", scoring->starts));
+  Kv8AttnArgs a{};
+  a.scored = true;
+  a.scale = scale * 1.44269504088896340736f;
+  if (cap != 0.0f) {
+    a.cap = cap * 1.44269504088896340736f;
+    a.scale *= 2.0f / cap;
+  }
+  a.slopes = scoring->slopes;
+  a.prefix_lens = scoring->prefix_lens;
+  a.starts = scoring->starts;
+  return kv8_attention_checked(fn, a, cache, batch, Q, dtype, q_heads, q_stride, scale, window, sinks, Y, workspace,
+                               workspace_bytes, stream);
 }
 
 qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_t* moves, hipStream_t stream) {

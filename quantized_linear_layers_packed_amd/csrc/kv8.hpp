@@ -94,6 +94,12 @@ struct Kv8AttnArgs {
   FastDiv by_group, by_heads, by_row_tiles, by_splits;
   int* counters;
   float* partials;
+  // other scores and masks (the kernels' SCORED form)
+  bool scored;
+  float cap;                    // times log2(e); 0: none.  `scale` is then 2 log2(e) scale / cap
+  const float* slopes;          // of the query heads; NULL: none
+  const int32_t* prefix_lens;   // of the sequences
+  const int32_t* starts;        // of the tokens
 };
 
 // The book of a cache's pages with the sizes that the host has checked.

@@ -98,7 +98,7 @@ constexpr size_t kPartial = 16 * NT * (D + 2);
 // lines (of pages of 128 tokens it takes every other half line): 131072 tokens of
 // 8 heads 54 -> 50 us, but 32 x 8192 tokens in pages of 128 99 -> 111 us.  K's
 // lines are shared by two loads each and stay cached.
-template <int D, int NT, int W, bool BF16, bool STREAM>
+template <int D, int NT, int W, bool BF16, bool STREAM, bool SCORED>
 __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(const Kv8AttnArgs a) {
   constexpr int KU = D / 64, DT = D / 16;
   __shared__ __align__(16) float sums[W][16][D + 4];
@@ -116,7 +116,9 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
   for (int r0 = (unit - rank * a.row_tiles) * (16 * NT); r0 < rows; r0 += a.row_tiles * (16 * NT)) {
     const int nrows = min(rows - r0, 16 * NT);
     const int p0 = seq.start + a.by_group(r0), p1 = seq.start + a.by_group(r0 + nrows - 1);
-    const Kv8Tiles tiles(p0, p1, a.window, a.sinks);
+    const Kv8Sight sight = SCORED ? Kv8Sight(a.prefix_lens, a.starts, a.sinks, b, seq, p0 - seq.start, p1 - seq.start) : Kv8Sight{};
+    const Kv8Tiles tiles = SCORED ? Kv8Tiles(p0, p1, a.window, a.sinks, sight)
+                                  : Kv8Tiles(p0, p1, a.window, a.sinks);
     // row tiles beyond those planned for are not split: their partial results
     // would share workspace with the first ones'
     const bool planned = r0 < a.row_tiles * (16 * NT);
@@ -128,6 +130,8 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
     h8_t qf[NT][KU][2];
     float cq[NT], m[NT], l[NT];
     int pos[NT], low[NT];                    // visible: j <= pos and (j >= low or j < sinks)
+    int start[NT], last[NT], kept[NT];       // SCORED: start <= j <= last and (j >= low or j < kept)
+    float slope[NT];                         // times -log2(e)
     f32x4_t o[NT][DT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -136,6 +140,12 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
       cq[n] *= a.scale;
       pos[n] = seq.start + t;
       low[n] = a.window > 0 ? max(pos[n], 0) - a.window + 1 : 0;
+      if constexpr (SCORED) {
+        start[n] = a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0;
+        last[n] = sight.last(pos[n]);
+        kept[n] = start[n] + min(a.sinks, seq.len - start[n]);
+        slope[n] = a.slopes ? a.slopes[h] * -1.44269504088896340736f : 0.0f;
+      }
       m[n] = kNone;
       l[n] = 0.0f;
 #pragma unroll
@@ -215,19 +225,38 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
         load_k(x + W, coming);
 
         // every position of the tile visible to every row, and every page there
-        const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && !__any(!here);
+        const bool full = (SCORED ? base + kTile - 1 <= sight.last(p0) && base >= sight.start1 &&
+                                        (base >= low_most || base + kTile <= sight.kept0)
+                                  : base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks)) && !__any(!here);
         const float vs = s.y < kLeastScale ? kLeastScale : s.y;                // NaN stays
         const float lv = __log2f(vs), iv = 1.0f / vs;
         h8_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float c = s.x * cq[n];
-          const uint32_t seen = full ? 0xFFFFu : visible_bits<16>(j0, pos[n], low[n], a.sinks, here);
+          const uint32_t seen = full ? 0xFFFFu
+                                : SCORED ? sight_bits<16>(j0, start[n], last[n], low[n], kept[n], here)
+                                         : visible_bits<16>(j0, pos[n], low[n], a.sinks, here);
           float top = seen != 0 ? kLowest : kNone;
+          if (SCORED && a.cap > 0.0f) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st[n][t][i] = fmaf(st[n][t][i], c, lv);
+              for (int i = 0; i < 4; ++i) st[n][t][i] = capped(st[n][t][i] * c, a.cap, lv);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st[n][t][i] = fmaf(st[n][t][i], c, lv);
+          }
+          if (SCORED && a.slopes) {
+            const float away = static_cast<float>(j0 - pos[n]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                st[n][t][i] = fmaf(slope[n], fabsf(away + static_cast<float>(4 * t + i)), st[n][t][i]);
+          }
           if (!full) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -363,8 +392,11 @@ template <int D, int NT, int W>
 void rows_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * W);
   const bool bf16 = dtype == QLIN_BF16, stream_v = a.c.log_page < 7;
-  const auto fn = bf16 ? (stream_v ? kv8_rows_kernel<D, NT, W, true, true> : kv8_rows_kernel<D, NT, W, true, false>)
-                       : (stream_v ? kv8_rows_kernel<D, NT, W, false, true> : kv8_rows_kernel<D, NT, W, false, false>);
+  const auto fn = a.scored
+      ? (bf16 ? (stream_v ? kv8_rows_kernel<D, NT, W, true, true, true> : kv8_rows_kernel<D, NT, W, true, false, true>)
+              : (stream_v ? kv8_rows_kernel<D, NT, W, false, true, true> : kv8_rows_kernel<D, NT, W, false, false, true>))
+      : (bf16 ? (stream_v ? kv8_rows_kernel<D, NT, W, true, true, false> : kv8_rows_kernel<D, NT, W, true, false, false>)
+              : (stream_v ? kv8_rows_kernel<D, NT, W, false, true, false> : kv8_rows_kernel<D, NT, W, false, false, false>));
   hipLaunchKernelGGL(fn, grid, block, 0, stream, a);
 }
 

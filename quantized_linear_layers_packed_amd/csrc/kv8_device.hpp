@@ -75,10 +75,42 @@ __device__ __forceinline__ uint32_t most_over_g(uint32_t v) {
   return most_over_32(max(static_cast<uint32_t>(r[0]), static_cast<uint32_t>(r[1])));
 }
 
+// What the kernels with other masks know of a row tile: the prefix that every query
+// of the sequence sees, the smallest and largest start of its rows' sights, and the
+// smallest and largest end of the first tokens there that stay visible.
+struct Kv8Sight {
+  int prefix = 0, start0 = 0, start1 = 0, kept0 = 0, kept1 = 0;
+  Kv8Sight() = default;
+  // tokens t0 .. t1 of the sequence; the same for every wave that asks
+  __device__ __forceinline__ Kv8Sight(const int32_t* prefix_lens, const int32_t* starts, int sinks, int b, const Kv8Seq& seq,
+                                      int t0, int t1) {
+    prefix = prefix_lens ? min(max(prefix_lens[b], 0), seq.len) : 0;
+    if (starts) {
+      int lo = 0x7FFFFFFF, hi = 0;
+      for (int t = t0 + static_cast<int>(threadIdx.x & 63); t <= t1; t += 64) {
+        const int s = min(max(starts[seq.row + t], 0), seq.len);
+        lo = min(lo, s);
+        hi = max(hi, s);
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) {
+        lo = min(lo, __shfl_xor(lo, off, 64));
+        hi = max(hi, __shfl_xor(hi, off, 64));
+      }
+      start0 = __builtin_amdgcn_readfirstlane(lo);
+      start1 = __builtin_amdgcn_readfirstlane(hi);
+    }
+    kept0 = start0 + min(sinks, seq.len - start0);         // (no sum passes the sequence's length)
+    kept1 = start1 + min(sinks, seq.len - start1);
+  }
+  // the last position that a query at pos sees
+  __device__ __forceinline__ int last(int pos) const { return pos < 0 ? -1 : max(pos, prefix - 1); }
+};
+
 // The tiles of 64 positions that the rows at positions p0 .. p1 see: those of the
 // first tokens and those from the start of the window of p0.
 struct Kv8Tiles {
-  int sinks, first, count;
+  int from = 0, sinks, first, count;
   __device__ __forceinline__ Kv8Tiles(int p0, int p1, int window, int sink_tokens) {
     if (p1 < 0) {
       sinks = first = count = 0;
@@ -88,8 +120,33 @@ struct Kv8Tiles {
     sinks = min(sink_tokens > 0 ? (sink_tokens - 1) / kTile + 1 : 0, first);
     count = sinks + p1 / kTile - first + 1;
   }
-  __device__ __forceinline__ int operator[](int x) const { return x < sinks ? x : first + x - sinks; }
+  // With sights of their own.
+  __device__ __forceinline__ Kv8Tiles(int p0, int p1, int window, int sink_tokens, const Kv8Sight& sight) {
+    const int last = sight.last(p1);
+    const bool any = p1 >= 0 && sight.start0 <= last;
+    from = sight.start0 / kTile;
+    first = max(window > 0 ? max(0, max(p0, 0) - window + 1) : 0, sight.start0) / kTile;
+    sinks = any && sink_tokens > 0 ? max(min((sight.kept1 - 1) / kTile + 1, first) - from, 0) : 0;
+    count = any ? sinks + last / kTile - first + 1 : 0;
+  }
+  __device__ __forceinline__ int operator[](int x) const { return x < sinks ? from + x : first + x - sinks; }
 };
+
+// Which of the N consecutive positions from j0 a row sees: those of start .. last that
+// lie from `low` on or before `kept`.
+template <int N>
+__device__ __forceinline__ uint32_t sight_bits(int j0, int start, int last, int low, int kept, bool held) {
+  const auto below = [&](int end) { return (1u << min(max(end - j0, 0), N)) - 1u; };
+  const uint32_t seen = below(last + 1) & ~below(start) & (~below(low) | below(kept));
+  return held ? seen : 0u;
+}
+
+// cap tanh(x / cap) in the exponent of two, plus `add`: cap - 2 cap / (e^(2 x / cap) + 1),
+// with z = 2 log2(e) x / cap and cap times log2(e).  Its error stays below 2^-21 cap: with
+// caps of up to 1024 less than 2^-11 of a weight.  Infinite x give +-cap.
+__device__ __forceinline__ float capped(float z, float cap, float add) {
+  return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.0f), cap + add);
+}
 
 // The sequence with the n-th most tiles (n from 0, ties to the lower index), found
 // by every wave for itself: a search down the bits of (tiles, 255 - index), a few

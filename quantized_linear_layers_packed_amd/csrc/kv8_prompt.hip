@@ -77,18 +77,24 @@ __device__ __forceinline__ void lookahead() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The kernel's forms: as it is, with other scores and masks, and these with capped scores.
+constexpr int kPlain = 0, kScored = 1, kCapped = 2;
+
 // A row tile: rows r0 .. r0 + nrows - 1 of a sequence, the tiles they see and how
 // many of them a split takes.  Row tiles beyond those planned for are not split:
 // their partial results would share workspace with the first ones'.
-template <int D>
+template <int D, int FORM>
 struct RowTile {
   static constexpr int ROWS = 32 * kPromptWaves<D>;
   int nrows, p0, p1;
+  Kv8Sight sight;
   Kv8Tiles tiles;
   int per, used;
-  __device__ __forceinline__ RowTile(const Kv8AttnArgs& a, const Kv8Seq& seq, int rows, int r0)
+  __device__ __forceinline__ RowTile(const Kv8AttnArgs& a, const Kv8Seq& seq, int b, int rows, int r0)
       : nrows(min(rows - r0, ROWS)), p0(seq.start + a.by_group(r0)), p1(seq.start + a.by_group(r0 + nrows - 1)),
-        tiles(p0, p1, a.window, a.sinks) {
+        sight(FORM ? Kv8Sight(a.prefix_lens, a.starts, a.sinks, b, seq, p0 - seq.start, p1 - seq.start) : Kv8Sight{}),
+        tiles(FORM ? Kv8Tiles(p0, p1, a.window, a.sinks, sight)
+                   : Kv8Tiles(p0, p1, a.window, a.sinks)) {
     const bool planned = r0 < a.row_tiles * ROWS;
     per = planned ? max(a.chunk, a.by_splits(tiles.count + a.splits - 1)) : max(tiles.count, 1);
     used = per >= tiles.count ? 1 : (tiles.count + per - 1) / per;
@@ -104,7 +110,7 @@ constexpr int kPromptSlot = kPromptWaves<D> * 64 * (D / 2 + 2);
 template <int SHARE>
 constexpr int kJoinThreads = SHARE > 4 ? 64 * SHARE : 256;
 
-template <int D, bool BF16>
+template <int D, bool BF16, int FORM>
 __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8_prompt_kernel(const Kv8AttnArgs a) {
   constexpr int W = kPromptWaves<D>, NT = 64 * W, ROWS = 32 * W, DT = D / 32, KS = D / 16;
   constexpr int NL = D * kTile / 16 / NT;                  // 16-byte pieces of K (and of V) per thread and tile
@@ -123,7 +129,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
   // Row tiles from the last, which sees the most, to the first; row tiles past
   // the grid are taken up in turn.
   for (int r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * ROWS; r0 < rows; r0 += a.row_tiles * ROWS) {
-    const RowTile<D> rt(a, seq, rows, r0);
+    const RowTile<D, FORM> rt(a, seq, b, rows, r0);
     const int nrows = rt.nrows, p0 = rt.p0, p1 = rt.p1;
     const Kv8Tiles& tiles = rt.tiles;
     if (split >= rt.used) continue;
@@ -134,6 +140,10 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
     const bool mine = 32 * wv + ql < nrows;
     const int pos = seq.start + t, low = a.window > 0 ? max(pos, 0) - a.window + 1 : 0;
     const int low_most = a.window > 0 ? max(p1, 0) - a.window + 1 : 0;
+    // (with other scores) this row sees start .. last, its first tokens end at `kept`; its slope times -log2(e)
+    const int start = FORM && a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0, last = FORM ? rt.sight.last(pos) : 0;
+    const int kept = FORM ? start + min(a.sinks, seq.len - start) : 0;
+    const float slope = FORM && a.slopes ? a.slopes[hq] * -1.44269504088896340736f : 0.0f;
     h8_t qf[KS];                                            // slice s: dimensions 16 s + 8 h .. + 7
     float cq = a.scale;
     {
@@ -251,10 +261,42 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
           iv[s] = run.iv;
         }
         const uint32_t held = __builtin_amdgcn_readfirstlane(now.held);
-        const bool full = base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks) && held == 15u;
+        const bool full = (FORM ? base + kTile - 1 <= rt.sight.last(p0) && base >= rt.sight.start1 &&
+                                      (base >= low_most || base + kTile <= rt.sight.kept0)
+                                : base + kTile - 1 <= p0 && (base >= low_most || base + kTile <= a.sinks)) && held == 15u;
         uint32_t seen[4];                                     // bit i of run s: this lane's token i
         float top = kLowest;
-        if (!full) {
+        if constexpr (FORM != kPlain) {
+          // scores with their value scale, capped and biased, as they go into the exponential
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x = st[s >> 1][8 * (s & 1) + i];
+              st[s >> 1][8 * (s & 1) + i] = FORM == kCapped ? capped(x * c[s], a.cap, lv[s]) : fmaf(x, c[s], lv[s]);
+            }
+          if (a.slopes) {
+            const float away = static_cast<float>(base + 8 * h - pos);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int k = 8 * (s & 1) + i;
+                st[s >> 1][k] = fmaf(slope, fabsf(away + static_cast<float>(16 * s + i)), st[s >> 1][k]);
+              }
+          }
+          if (!full) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              seen[s] = sight_bits<8>(base + 16 * s + 8 * h, start, last, low, kept, (held >> s) & 1u);
+              iv[s] = seen[s] != 0 ? iv[s] : 0.0f;            // scales of hidden pages may be anything, NaN among it
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                st[s >> 1][8 * (s & 1) + i] = (seen[s] >> i) & 1u ? st[s >> 1][8 * (s & 1) + i] : -INFINITY;
+            }
+            top = (seen[0] | seen[1] | seen[2] | seen[3]) != 0 ? kLowest : kNone;
+          }
+        } else if (!full) {
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             seen[s] = visible_bits<8>(base + 16 * s + 8 * h, pos, low, a.sinks, (held >> s) & 1u);
@@ -271,7 +313,7 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
           float mx = st[s >> 1][8 * (s & 1)];
 #pragma unroll
           for (int i = 1; i < 8; ++i) mx = fmaxf(mx, st[s >> 1][8 * (s & 1) + i]);
-          top = fmaxf(top, fmaf(mx, c[s], lv[s]));
+          top = fmaxf(top, FORM ? mx : fmaf(mx, c[s], lv[s]));
         }
         if (__any(top > m + kSlack)) {
           const float high = max_over_32(top), was = m;
@@ -287,10 +329,10 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int k = 8 * (s & 1) + i;
-            st[s >> 1][k] = __builtin_amdgcn_exp2f(fmaf(st[s >> 1][k], c[s], shift));
+            st[s >> 1][k] = __builtin_amdgcn_exp2f(FORM ? st[s >> 1][k] - m : fmaf(st[s >> 1][k], c[s], shift));
           }
         }
-        if (!full) {                                          // scales of hidden pages may be anything, NaN among it
+        if (FORM == kPlain && !full) {                                          // scales of hidden pages may be anything, NaN among it
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             iv[s] = seen[s] != 0 ? iv[s] : 0.0f;
@@ -358,16 +400,16 @@ __global__ __launch_bounds__(64 * kPromptWaves<D>, kPromptOccupancy<D>) void kv8
 // consecutive splits each.  What bounds it is the latency of its loads: with one
 // wave to a task 64 splits took 24.5 us, with sixteen, whose loads all leave at
 // once, 5 us.
-template <int D, int SHARE, bool BF16>
+template <int D, int SHARE, bool BF16, int FORM>
 __global__ __launch_bounds__(kJoinThreads<SHARE>) void kv8_prompt_join_kernel(const Kv8AttnArgs a) {
   constexpr int GROUPS = D / 8, AHEAD = 8;
   const int lane = threadIdx.x & 63, h = lane >> 5, ql = lane & 31, wave = threadIdx.x >> 6, member = wave % SHARE;
   const int task = blockIdx.y * (kJoinThreads<SHARE> / 64 / SHARE) + wave / SHARE, wv = task / GROUPS, group = task % GROUPS;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads, b = a.by_row_tiles(unit);
   const Kv8Seq seq = kv8_seq(a.c, b);
-  const int rows = seq.count * a.group, r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * RowTile<D>::ROWS;
+  const int rows = seq.count * a.group, r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * RowTile<D, FORM>::ROWS;
   if (r0 >= rows || rows < a.least_rows || rows > a.most_rows) return;
-  const RowTile<D> rt(a, seq, rows, r0);
+  const RowTile<D, FORM> rt(a, seq, b, rows, r0);
   if (rt.used == 1 || 32 * wv >= rt.nrows) return;          // (the same for all of a task)
   const float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.splits * kPromptSlot<D> + wv * 64 * (D / 2 + 2) + lane;
   const int each = (rt.used + SHARE - 1) / SHARE, k1 = min(rt.used, (member + 1) * each);
@@ -429,7 +471,10 @@ template <int D, int SHARE>
 void join_launch(const Kv8AttnArgs& a, int dtype, unsigned units, hipStream_t stream) {
   constexpr int kTasks = kPromptWaves<D> * (D / 8);
   const dim3 grid(units, kTasks / (kJoinThreads<SHARE> / 64 / SHARE)), block(kJoinThreads<SHARE>);
-  const auto fn = dtype == QLIN_BF16 ? kv8_prompt_join_kernel<D, SHARE, true> : kv8_prompt_join_kernel<D, SHARE, false>;
+  const auto fn = a.scored ? (dtype == QLIN_BF16 ? kv8_prompt_join_kernel<D, SHARE, true, kScored>
+                                                 : kv8_prompt_join_kernel<D, SHARE, false, kScored>)
+                           : (dtype == QLIN_BF16 ? kv8_prompt_join_kernel<D, SHARE, true, kPlain>
+                                                 : kv8_prompt_join_kernel<D, SHARE, false, kPlain>);
   hipLaunchKernelGGL(fn, grid, block, 0, stream, a);
 }
 
@@ -437,7 +482,10 @@ template <int D>
 void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads, a.splits), block(64 * kPromptWaves<D>);
   const size_t lds = 2 * sizeof(Tile16<D>);
-  const auto fn = dtype == QLIN_BF16 ? kv8_prompt_kernel<D, true> : kv8_prompt_kernel<D, false>;
+  const bool bf16 = dtype == QLIN_BF16;
+  const auto fn = !a.scored ? (bf16 ? kv8_prompt_kernel<D, true, kPlain> : kv8_prompt_kernel<D, false, kPlain>)
+                  : a.cap > 0.0f ? (bf16 ? kv8_prompt_kernel<D, true, kCapped> : kv8_prompt_kernel<D, false, kCapped>)
+                                 : (bf16 ? kv8_prompt_kernel<D, true, kScored> : kv8_prompt_kernel<D, false, kScored>);
   hipLaunchKernelGGL(fn, grid, block, lds, stream, a);
   if (a.splits > 32) join_launch<D, 16>(a, dtype, grid.x, stream);
   else if (a.splits > 8) join_launch<D, 4>(a, dtype, grid.x, stream);

@@ -50,7 +50,7 @@ EXPORTS = (
     "qlin_w4_workspace_bytes", "sq_int8_gemm_workspace_bytes", "qlin_w4_forward_scratch",
     "qlin_mfma_peak", "spqr_workspace_bytes", "qlin_f16_gemm", "qlin_f16_gemm_workspace_bytes",
     "qlin_kv8_sizes", "qlin_kv8_append", "qlin_kv8_gather", "qlin_kv8_attention", "qlin_kv8_attention_workspace_bytes",
-    "qlin_kv8_grow", "qlin_kv8_fork", "qlin_kv8_free", "qlin_kv8_compact", "qlin_kv8_copy_pages",
+    "qlin_kv8_attention_scored", "qlin_kv8_grow", "qlin_kv8_fork", "qlin_kv8_free", "qlin_kv8_compact", "qlin_kv8_copy_pages",
 )
 
 _vp, _i, _i64, _sz, _d, _f = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_double, C.c_float
@@ -90,6 +90,7 @@ _sigs = {
     "qlin_kv8_gather": ([_vp, _vp, _vp, _vp, _i, _vp], _i),
     "qlin_kv8_attention": ([_vp, _vp, _vp, _i, _i, _i64, _f, _i, _i, _vp, _vp, _sz, _vp], _i),
     "qlin_kv8_attention_workspace_bytes": ([_vp, _vp, _i, _i, _i, _vp], _i),
+    "qlin_kv8_attention_scored": ([_vp, _vp, _vp, _i, _i, _i64, _f, _i, _i, _vp, _vp, _vp, _sz, _vp], _i),
     "qlin_kv8_grow": ([_vp, _vp, _vp, _vp], _i),
     "qlin_kv8_fork": ([_vp, _vp, _vp, _vp, _i, _vp, _vp], _i),
     "qlin_kv8_free": ([_vp, _vp, _vp, _vp, _i, _vp], _i),
@@ -446,7 +447,7 @@ class Kv8Batch:
         self.tensors = (offsets, kv_lens, block_table)
         self._c = _KvBatch(_ptr(offsets), _ptr(kv_lens), _ptr(block_table), seqs, tokens, stride, max_new, max_kv)
         self.ref = C.addressof(self._c)
-        self.tokens = tokens
+        self.tokens, self.seqs = tokens, seqs
 
 
 def _rows(x, tokens, heads, dim, types):
@@ -516,6 +517,39 @@ def qlin_kv8_attention(cache, batch, Q, dtype, q_heads, scale, window, sinks, Y,
     _check(_lib.qlin_kv8_attention(cache.ref, batch.ref, q, dtype, q_heads, q_stride, scale, window, sinks,
                                    _out(Y, T, q_heads, D, half), _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                    _stream(stream)))
+
+
+class _KvScoring(C.Structure):
+    _fields_ = [("cap", C.c_float), ("slopes", _vp), ("prefix_lens", _vp), ("starts", _vp)]
+
+
+class Kv8Scoring:
+    """A qlin_kv8_scoring: cap (0: none), slopes fp32 [q_heads], prefix_lens int32 [seqs], starts int32 [tokens], each of
+    them None for none.  Keeps the tensors alive; their contents may change between calls."""
+
+    def __init__(self, cap=0.0, slopes=None, prefix_lens=None, starts=None):
+        for name, t, types in (("slopes", slopes, _F32), ("prefix_lens", prefix_lens, _INDICES), ("starts", starts, _INDICES)):
+            if t is not None:
+                if len(t.shape) != 1:
+                    raise ValueError(f"{name}: one dimension expected, got shape {tuple(t.shape)}")
+                _typed(name, t, types)
+        self.tensors = (slopes, prefix_lens, starts)
+        self._c = _KvScoring(cap, _ptr(slopes), _ptr(prefix_lens), _ptr(starts))
+        self.ref = C.addressof(self._c)
+
+
+def qlin_kv8_attention_scored(cache, batch, Q, dtype, q_heads, scale, window, sinks, scoring, Y, workspace=None,
+                              workspace_bytes=None, stream=None):
+    """As qlin_kv8_attention (its workspace too), with a Kv8Scoring whose tensors fit the batch."""
+    T, D = batch.tokens, cache.head_dim
+    half = _HALF.get(dtype, _ANY)
+    for name, t, n in zip(("slopes", "prefix_lens", "starts"), scoring.tensors, (q_heads, batch.seqs, T)):
+        if t is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: [{n}] expected, got shape {tuple(t.shape)}")
+    q, q_stride = _rows(Q, T, q_heads, D, half)
+    _check(_lib.qlin_kv8_attention_scored(cache.ref, batch.ref, q, dtype, q_heads, q_stride, scale, window, sinks, scoring.ref,
+                                          _out(Y, T, q_heads, D, half), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                          _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
