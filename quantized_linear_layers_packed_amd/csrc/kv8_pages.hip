@@ -31,7 +31,7 @@ constexpr int kStep = kThreads * kEach;
 __device__ __forceinline__ bool is_page(int page, int pages) { return static_cast<unsigned>(page) < static_cast<unsigned>(pages); }
 
 // Sum of v over the threads before this one, and over all in *total.
-// part: 17 ints in LDS, free again when the call returns.
+// part: 16 ints in LDS, free again when the call returns.
 __device__ __forceinline__ int sum_before(int v, int* part, int* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int up = v;
@@ -54,53 +54,79 @@ __device__ __forceinline__ int sum_before(int v, int* part, int* total) {
   return before;
 }
 
-// Which of the 16 pages from `first` on (a multiple of 16; it may lie past the pool's end) are free, as bits.
-__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int pages, int first) {
+// The pages of a step are dealt out 1024 to a wave, in 16 rows of 64: lane l's i-th is
+// first + 64 i + l, so that loads, and what is written for pages in turn, are
+// consecutive over the lanes.  Bit i: that page lies before `end` (which is above
+// 0) and is free.
+__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int at, int end) {
+  const int first = at + (threadIdx.x & ~63) * kEach + (threadIdx.x & 63);
+  int r[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) r[i] = refs[min(first + 64 * i, end - 1)];
   uint32_t bits = 0;
-  if (first + kEach <= pages) {
-    int4 r[kEach / 4];
 #pragma unroll
-    for (int i = 0; i < kEach / 4; ++i) r[i] = reinterpret_cast<const int4*>(refs + first)[i];
-#pragma unroll
-    for (int i = 0; i < kEach / 4; ++i) {
-      bits |= static_cast<uint32_t>(r[i].x <= 0) << (4 * i) | static_cast<uint32_t>(r[i].y <= 0) << (4 * i + 1) |
-              static_cast<uint32_t>(r[i].z <= 0) << (4 * i + 2) | static_cast<uint32_t>(r[i].w <= 0) << (4 * i + 3);
-    }
-  } else {
-    for (int i = 0; i < pages - first; ++i) bits |= static_cast<uint32_t>(refs[first + i] <= 0) << i;
-  }
+  for (int i = 0; i < kEach; ++i) bits |= static_cast<uint32_t>(r[i] <= 0 && first + 64 * i < end) << i;
   return bits;
 }
-__device__ __forceinline__ int pages_of(int pages, int first) { return min(max(pages - first, 0), kEach); }
+__device__ __forceinline__ int wave_count(uint32_t bits) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) n += __popcll(__ballot((bits >> i) & 1u));
+  return n;
+}
+// Sum over the waves before this one of a number that is the same in all of a wave's
+// lanes, and over all waves in *total.
+__device__ __forceinline__ int waves_before(int n, int* part, int* total) {
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) part[wave] = n;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    const int p = part[w];
+    before += w < wave ? p : 0;
+    all += p;
+  }
+  *total = all;
+  __syncthreads();
+  return before;
+}
+// give(rank, page) for the pages of a step that `bits` names, `rank` being that of the
+// wave's first, until `limit`.
+template <class Give>
+__device__ __forceinline__ void each_page(uint32_t bits, int at, int rank, int limit, Give give) {
+  const int lane = threadIdx.x & 63, first = at + (threadIdx.x & ~63) * kEach + lane;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint64_t all = __ballot((bits >> i) & 1u);
+    const int mine = rank + __popcll(all & ((uint64_t{1} << lane) - 1));
+    if (((bits >> i) & 1u) && mine < limit) give(mine, first + 64 * i);
+    rank += __popcll(all);
+  }
+}
 
 // give(rank, page) for the `wanted` lowest free pages in turn, if there are as many;
 // returns how many are missing (the same in every thread).  Nothing is given then.
+// ahead: free_bits of the first step, asked for before it was known how many pages
+// are wanted.
 template <class Give>
-__device__ __forceinline__ int take_free(const int32_t* refs, int pages, int wanted, int* part, Give give) {
-  int found = 0, steps = 0;
-  uint32_t bits = 0;
-  int before = 0;
+__device__ __forceinline__ int take_free(const int32_t* refs, int pages, int wanted, uint32_t ahead, int* part, Give give) {
+  int found = 0, steps = 0, before = 0;
   for (int at = 0; at < pages && found < wanted; at += kStep, ++steps) {
-    bits = free_bits(refs, pages, at + static_cast<int>(threadIdx.x) * kEach);
     int total;
-    before = found + sum_before(__popc(bits), part, &total);
+    before = found + waves_before(wave_count(at == 0 ? ahead : free_bits(refs, at, pages)), part, &total);
     found += total;
   }
   if (found < wanted) return wanted - found;
   // every count has been read: what follows may change them
   for (int s = 0, have = 0; s < steps; ++s) {
-    const int first = s * kStep + static_cast<int>(threadIdx.x) * kEach;
+    const uint32_t bits = s == 0 ? ahead : free_bits(refs, s * kStep, pages);
     if (steps > 1) {
-      bits = free_bits(refs, pages, first);
       int total;
-      before = have + sum_before(__popc(bits), part, &total);
+      before = have + waves_before(wave_count(bits), part, &total);
       have += total;
     }
-    for (int rank = before; bits != 0 && rank < wanted; ++rank) {
-      const int i = __ffs(bits) - 1;
-      bits &= bits - 1;
-      give(rank, first + i);
-    }
+    if (before < wanted) each_page(bits, s * kStep, before, wanted, give);
   }
   return 0;
 }
@@ -119,11 +145,12 @@ __device__ __forceinline__ int entries_of(int len, const Kv8Book& k) {
 __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, const int32_t* __restrict__ lens,
                                                             int2* __restrict__ moves) {
   extern __shared__ int start[];               // [rows + 1]: wanted pages before each row; before that the needs
-  __shared__ int part[17];
+  __shared__ int part[kThreads / 64];
   __shared__ int bad, searched;
   const int tid = threadIdx.x, lane = tid & 63;
   if (tid == 0) bad = searched = 0;
   __syncthreads();
+  const uint32_t ahead = free_bits(k.refs, 0, k.pages);
   for (int b = tid; b < k.rows; b += kThreads) {
     const int want = entries_of(lens[b], k);
     const int32_t* row = k.table + static_cast<size_t>(b) * k.stride;
@@ -174,15 +201,21 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
   }
   if (tid == 0) start[k.rows] = total;
   __syncthreads();
-  const int missing = total == 0 ? 0 : take_free(k.refs, k.pages, total, part, [&](int rank, int page) {
-    int lo = 0, hi = k.rows;                   // the row whose places hold the rank: start[lo] <= rank < start[lo + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (start[mid] <= rank) lo = mid;
-      else hi = mid;
+  // the row whose places hold a rank, start[row] <= rank < start[row + 1], and where its
+  // entries end: a thread's ranks ascend, and often stay in the row
+  int row = -1, want = 0;
+  const int missing = total == 0 ? 0 : take_free(k.refs, k.pages, total, ahead, part, [&](int rank, int page) {
+    if (row < 0 || start[row + 1] <= rank) {
+      int lo = row < 0 ? 0 : row + 1, hi = k.rows;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= rank) lo = mid;
+        else hi = mid;
+      }
+      row = lo;
+      want = entries_of(lens[row], k);
     }
-    const int want = entries_of(lens[lo], k);
-    k.table[static_cast<size_t>(lo) * k.stride + want - (start[lo + 1] - rank)] = page;
+    k.table[static_cast<size_t>(row) * k.stride + want - (start[row + 1] - rank)] = page;
     k.refs[page] = 1;
   });
   if (tid == 0) moves[0] = make_int2(missing ? 0 : total, missing);
@@ -195,11 +228,12 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_plan_kernel(const Kv8Book k
                                                                  const int32_t* __restrict__ lens, int n,
                                                                  int2* __restrict__ moves) {
   extern __shared__ int held[];                // fresh pages by rank [n], then rows that are children, and parents, as bits
-  __shared__ int part[17];
+  __shared__ int part[kThreads / 64];
   __shared__ int bad;
   const int tid = threadIdx.x, words = (k.rows + 31) / 32;
   int* is_child = held + n;
   int* is_parent = is_child + words;
+  const uint32_t ahead = free_bits(k.refs, 0, k.pages);
   for (int i = tid; i < 2 * words; i += kThreads) is_child[i] = 0;
   if (tid == 0) bad = 0;
   __syncthreads();
@@ -232,7 +266,7 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_plan_kernel(const Kv8Book k
   int mine = 0, total;
   for (int i = i0; i < i1; ++i) mine += source(i) >= 0;
   int rank = sum_before(mine, part, &total);
-  const int missing = total == 0 ? 0 : take_free(k.refs, k.pages, total, part, [&](int r, int page) {
+  const int missing = total == 0 ? 0 : take_free(k.refs, k.pages, total, ahead, part, [&](int r, int page) {
     held[r] = page;
     k.refs[page] = 1;
   });
@@ -244,82 +278,131 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_plan_kernel(const Kv8Book k
   if (tid == 0) moves[0] = make_int2(missing ? 0 : n, missing);
 }
 
+// Adds to the counts of pages, summed while the page stays the same: neighbours in a
+// list often share theirs (forks of one prefix: 64 children of 2 parents each way took
+// 8.6 us with an addition for every child).
+struct Counts {
+  int32_t* refs;
+  int page = -1, by = 0;
+  __device__ __forceinline__ void add(int p, int n) {
+    if (p != page) {
+      flush();
+      page = p;
+      by = 0;
+    }
+    by += n;
+  }
+  __device__ __forceinline__ void flush() {
+    if (page >= 0 && by != 0) atomicAdd(refs + page, by);
+  }
+};
+constexpr int kListEach = 8;                  // of a list, to a workgroup
+
 // The children's rows: shared pages, the fresh one, nothing behind; what they held
 // before goes back.  Grid: entries x children.
 __global__ __launch_bounds__(256) void kv8_fork_rows_kernel(const Kv8Book k, const int32_t* __restrict__ parents,
                                                             const int32_t* __restrict__ children,
-                                                            const int32_t* __restrict__ lens,
+                                                            const int32_t* __restrict__ lens, int n,
                                                             const int2* __restrict__ moves) {
-  const int i = blockIdx.y, p = parents[i], c = children[i];
-  const int2 head = moves[0], move = moves[1 + i];
-  if (head.y != 0 || p < 0 || c < 0) return;
-  const int len = lens[i], full = len >> k.log_page;
-  const int32_t* from = k.table + static_cast<size_t>(p) * k.stride;
-  int32_t* to = k.table + static_cast<size_t>(c) * k.stride;
+  const int i0 = blockIdx.y * kListEach;
+  const int short_by = moves[0].y;
+  int p[kListEach], c[kListEach], len[kListEach], fresh[kListEach];
+#pragma unroll
+  for (int j = 0; j < kListEach; ++j) {
+    const int i = min(i0 + j, n - 1);
+    p[j] = parents[i];
+    c[j] = i0 + j < n ? children[i] : -1;
+    len[j] = lens[i];
+    fresh[j] = moves[1 + i].y;
+  }
+  if (short_by != 0) return;                   // (lists that do not fit the table among it)
   for (int e = blockIdx.x * 256 + threadIdx.x; e < k.stride; e += gridDim.x * 256) {
-    const int was = to[e], theirs = e < full ? from[e] : -1;
-    const int shared = is_page(theirs, k.pages) ? theirs : -1, now = e == full ? move.y : shared;
-    if (now == was) continue;                  // (never the fresh page: that one was free)
-    if (shared >= 0) atomicAdd(k.refs + shared, 1);
-    if (is_page(was, k.pages)) atomicSub(k.refs + was, 1);
-    to[e] = now;
+    int was[kListEach], theirs[kListEach];
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j) {
+      was[j] = theirs[j] = -1;
+      if (p[j] < 0 || c[j] < 0) continue;      // padding
+      was[j] = k.table[static_cast<size_t>(c[j]) * k.stride + e];
+      if (e < len[j] >> k.log_page) theirs[j] = k.table[static_cast<size_t>(p[j]) * k.stride + e];
+    }
+    Counts more{k.refs}, fewer{k.refs};
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j) {
+      if (p[j] < 0 || c[j] < 0) continue;
+      const int shared = is_page(theirs[j], k.pages) ? theirs[j] : -1, now = e == len[j] >> k.log_page ? fresh[j] : shared;
+      if (now == was[j]) continue;             // (never the fresh page: that one was free)
+      if (shared >= 0) more.add(shared, 1);
+      if (is_page(was[j], k.pages)) fewer.add(was[j], -1);
+      k.table[static_cast<size_t>(c[j]) * k.stride + e] = now;
+    }
+    more.flush();
+    fewer.flush();
   }
 }
 
 // Gives back the entries whose tokens all lie in begin .. end-1.  An entry is taken
 // by an exchange, so that rows named twice give their pages back once.
 __global__ __launch_bounds__(256) void kv8_free_kernel(const Kv8Book k, const int32_t* __restrict__ rows,
-                                                       const int32_t* __restrict__ begin, const int32_t* __restrict__ end) {
-  const int i = blockIdx.y, b = rows[i], P = 1 << k.log_page;
-  if (!is_page(b, k.rows)) return;             // padding
-  int e0 = 0, e1 = k.stride;
-  if (begin) {
-    const int t = max(begin[i], 0);
-    e0 = (t >> k.log_page) + ((t & (P - 1)) != 0);
+                                                       const int32_t* __restrict__ begin, const int32_t* __restrict__ end, int n) {
+  const int i0 = blockIdx.y * kListEach, P = 1 << k.log_page;
+  int b[kListEach], e0[kListEach], e1[kListEach];
+#pragma unroll
+  for (int j = 0; j < kListEach; ++j) {
+    const int i = min(i0 + j, n - 1), t = begin ? max(begin[i], 0) : 0;
+    b[j] = rows[i];
+    e0[j] = (t >> k.log_page) + ((t & (P - 1)) != 0);
+    e1[j] = end ? min(max(end[i], 0) >> k.log_page, k.stride) : k.stride;
+    if (i0 + j >= n || !is_page(b[j], k.rows)) e1[j] = 0;      // past the list, or padding
   }
-  if (end) e1 = min(max(end[i], 0) >> k.log_page, k.stride);
-  int32_t* row = k.table + static_cast<size_t>(b) * k.stride;
-  for (int e = e0 + blockIdx.x * 256 + threadIdx.x; e < e1; e += gridDim.x * 256) {
-    if (row[e] == -1) continue;
-    const int was = atomicExch(row + e, -1);
-    if (is_page(was, k.pages)) atomicSub(k.refs + was, 1);
+  int first = e0[0], last = e1[0];
+#pragma unroll
+  for (int j = 1; j < kListEach; ++j) {
+    first = min(first, e0[j]);
+    last = max(last, e1[j]);
+  }
+  for (int e = first + blockIdx.x * 256 + threadIdx.x; e < last; e += gridDim.x * 256) {
+    int was[kListEach];
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j)
+      was[j] = e >= e0[j] && e < e1[j] ? k.table[static_cast<size_t>(b[j]) * k.stride + e] : -1;
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j)
+      if (was[j] != -1) was[j] = atomicExch(k.table + static_cast<size_t>(b[j]) * k.stride + e, -1);
+    Counts fewer{k.refs};
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j)
+      if (is_page(was[j], k.pages)) fewer.add(was[j], -1);
+    fewer.flush();
   }
 }
 
 // The moves of a compaction: with U pages in use, every free page below U gets one of
 // the used pages from U on, the lowest the highest; at most `most` of them.
 __global__ __launch_bounds__(kThreads) void kv8_compact_plan_kernel(const Kv8Book k, int most, int2* __restrict__ moves) {
-  __shared__ int part[17];
+  __shared__ int part[kThreads / 64];
   const int tid = threadIdx.x;
-  int total;
-  int unused = 0;
-  for (int at = 0; at < k.pages; at += kStep) unused += __popc(free_bits(k.refs, k.pages, at + tid * kEach));
-  sum_before(unused, part, &total);
+  int total, unused = 0;
+  for (int at = 0; at < k.pages; at += kStep) unused += wave_count(free_bits(k.refs, at, k.pages));
+  waves_before(unused, part, &total);
   const int used = k.pages - total;
   int low = 0;                                 // free pages below `used`: as many as there are used ones from there on
   for (int at = 0; at < used; at += kStep) {
-    const int first = at + tid * kEach;
-    uint32_t bits = free_bits(k.refs, k.pages, first) & ((1u << pages_of(used, first)) - 1u);
-    int rank = low + sum_before(__popc(bits), part, &total);
+    const uint32_t bits = free_bits(k.refs, at, used);
+    const int rank = low + waves_before(wave_count(bits), part, &total);
     low += total;
-    for (; bits != 0 && rank < most; ++rank) {
-      const int i = __ffs(bits) - 1;
-      bits &= bits - 1;
-      moves[1 + rank].y = first + i;
-    }
+    each_page(bits, at, rank, most, [&](int r, int page) { moves[1 + r].y = page; });
   }
   for (int at = used, have = 0; at < k.pages && have < low; at += kStep) {
-    // (from a page that need not be a multiple of four: word by word)
-    const int first = at + tid * kEach, n = pages_of(k.pages, first);
-    uint32_t bits = 0;
-    for (int i = 0; i < n; ++i) bits |= static_cast<uint32_t>(k.refs[first + i] > 0) << i;
-    int rank = low - 1 - (have + sum_before(__popc(bits), part, &total));
+    const uint32_t bits = free_bits(k.refs, at, k.pages);
+    uint32_t there = 0;                        // pages of the pool
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      there |= static_cast<uint32_t>(at + (tid & ~63) * kEach + 64 * i + (tid & 63) < k.pages) << i;
+    const int rank = have + waves_before(wave_count(there & ~bits), part, &total);
     have += total;
-    for (; bits != 0; --rank) {
-      const int i = __ffs(bits) - 1;
-      bits &= bits - 1;
-      if (rank < most) moves[1 + rank].x = first + i;
-    }
+    each_page(there & ~bits, at, rank, low, [&](int r, int page) {
+      if (low - 1 - r < most) moves[1 + low - 1 - r].x = page;
+    });
   }
   const int count = min(low, most);
   for (int i = count + tid; i < most; i += kThreads) moves[1 + i] = make_int2(-1, -1);
@@ -333,22 +416,37 @@ __global__ __launch_bounds__(kThreads) void kv8_compact_plan_kernel(const Kv8Boo
 }
 
 // The table after the moves: an entry from the lowest moved page on is looked up
-// among them (their sources descend).
+// among them (their sources descend), in a copy in LDS of all of them or of every
+// 2^s-th, and from there in the list itself.
+constexpr int kSamples = 4096;
 __global__ __launch_bounds__(256) void kv8_compact_rows_kernel(const Kv8Book k, const int2* __restrict__ moves) {
+  __shared__ int sample[kSamples];
   const int count = moves[0].x;
   if (count == 0) return;
+  int shift = 0;
+  while ((count - 1) >> shift >= kSamples) ++shift;
+  const int samples = ((count - 1) >> shift) + 1;
+  for (int i = threadIdx.x; i < samples; i += 256) sample[i] = moves[1 + (i << shift)].x;
   const int lowest = moves[count].x;
+  __syncthreads();
   const long long entries = static_cast<long long>(k.rows) * k.stride;
   for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < entries; e += static_cast<long long>(gridDim.x) * 256) {
     const int page = k.table[e];
     if (page < lowest || !is_page(page, k.pages)) continue;
-    int lo = 1, hi = count;                    // the last move whose source is at least the page
+    int lo = 0, hi = samples - 1;              // the last of them whose source is at least the page
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (moves[mid].x >= page) lo = mid;
+      if (sample[mid] >= page) lo = mid;
       else hi = mid - 1;
     }
-    const int2 m = moves[lo];
+    lo <<= shift;
+    hi = min(lo + (1 << shift), count) - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (moves[1 + mid].x >= page) lo = mid;
+      else hi = mid - 1;
+    }
+    const int2 m = moves[1 + lo];
     if (m.x == page) k.table[e] = m.y;
   }
 }
@@ -358,30 +456,33 @@ __global__ __launch_bounds__(256) void kv8_compact_rows_kernel(const Kv8Book k, 
 constexpr int kCopyEach = 4;
 __global__ __launch_bounds__(256) void kv8_copy_kernel(const Kv8CopyArgs a) {
   const Kv8CopyLayer l = a.layers[blockIdx.z];
-  const int count = min(a.moves[0].x, a.most);
   const int half = a.chunks, first = blockIdx.x * (256 * kCopyEach) + threadIdx.x;
-  for (int m = blockIdx.y; m < count; m += gridDim.y) {
-    const int2 move = a.moves[1 + m];
-    if (!is_page(move.x, a.from_pages) || !is_page(move.y, a.to_pages)) continue;
-    const uint4* k = reinterpret_cast<const uint4*>(l.from_k) + static_cast<size_t>(move.x) * half;
-    const uint4* v = reinterpret_cast<const uint4*>(l.from_v) + static_cast<size_t>(move.x) * half;
-    uint4* k_to = reinterpret_cast<uint4*>(l.to_k) + static_cast<size_t>(move.y) * half;
-    uint4* v_to = reinterpret_cast<uint4*>(l.to_v) + static_cast<size_t>(move.y) * half;
-    uint4 w[kCopyEach];                        // (chunks past the end: the last one, not stored)
+  int2 move = a.moves[1 + blockIdx.y];         // (there, also where it is not counted)
+  const int count = min(a.moves[0].x, a.most);
+  for (int m = blockIdx.y; m < count;) {
+    if (is_page(move.x, a.from_pages) && is_page(move.y, a.to_pages)) {
+      const u32x4_t* k = reinterpret_cast<const u32x4_t*>(l.from_k) + static_cast<size_t>(move.x) * half;
+      const u32x4_t* v = reinterpret_cast<const u32x4_t*>(l.from_v) + static_cast<size_t>(move.x) * half;
+      u32x4_t* k_to = reinterpret_cast<u32x4_t*>(l.to_k) + static_cast<size_t>(move.y) * half;
+      u32x4_t* v_to = reinterpret_cast<u32x4_t*>(l.to_v) + static_cast<size_t>(move.y) * half;
+      const float2* s = l.from_scales + static_cast<size_t>(move.x) * a.heads;
+      float2* s_to = l.to_scales + static_cast<size_t>(move.y) * a.heads;
+      u32x4_t w[kCopyEach];                    // (chunks past the end: the last one, not stored)
 #pragma unroll
-    for (int i = 0; i < kCopyEach; ++i) {
-      const int c = min(first + 256 * i, 2 * half - 1);
-      w[i] = *(c < half ? k + c : v + (c - half));
-    }
+      for (int i = 0; i < kCopyEach; ++i) {
+        const int c = min(first + 256 * i, 2 * half - 1);
+        w[i] = *(c < half ? k + c : v + (c - half));
+      }
+      if (blockIdx.x == 0)
+        for (int h = threadIdx.x; h < a.heads; h += 256) s_to[h] = s[h];
 #pragma unroll
-    for (int i = 0; i < kCopyEach; ++i) {
-      const int c = first + 256 * i;
-      if (c < half) k_to[c] = w[i];
-      else if (c < 2 * half) v_to[c - half] = w[i];
+      for (int i = 0; i < kCopyEach; ++i) {
+        const int c = first + 256 * i;
+        if (c < 2 * half) *(c < half ? k_to + c : v_to + (c - half)) = w[i];
+      }
     }
-    if (blockIdx.x == 0)
-      for (int h = threadIdx.x; h < a.heads; h += 256)
-        l.to_scales[static_cast<size_t>(move.y) * a.heads + h] = l.from_scales[static_cast<size_t>(move.x) * a.heads + h];
+    m += gridDim.y;
+    if (m < count) move = a.moves[1 + m];
   }
 }
 
@@ -399,12 +500,13 @@ void kv8_fork_launch(const Kv8Book& k, const int32_t* parents, const int32_t* ch
   int2* m = reinterpret_cast<int2*>(moves);
   const size_t lds = sizeof(int) * (n + 2 * ((k.rows + 31) / 32));
   hipLaunchKernelGGL(kv8_fork_plan_kernel, dim3(1), dim3(kThreads), lds, stream, k, parents, children, lens, n, m);
-  hipLaunchKernelGGL(kv8_fork_rows_kernel, dim3(chunks_of(k.stride, 256, 64), n), dim3(256), 0, stream, k, parents, children,
-                     lens, static_cast<const int2*>(m));
+  hipLaunchKernelGGL(kv8_fork_rows_kernel, dim3(chunks_of(k.stride, 256, 64), chunks_of(n, kListEach, n)), dim3(256), 0, stream,
+                     k, parents, children, lens, n, static_cast<const int2*>(m));
 }
 
 void kv8_free_launch(const Kv8Book& k, const int32_t* rows, const int32_t* begin, const int32_t* end, int n, hipStream_t stream) {
-  hipLaunchKernelGGL(kv8_free_kernel, dim3(chunks_of(k.stride, 1024, 64), n), dim3(256), 0, stream, k, rows, begin, end);
+  hipLaunchKernelGGL(kv8_free_kernel, dim3(chunks_of(k.stride, 256, 64), chunks_of(n, kListEach, n)), dim3(256), 0, stream, k, rows,
+                     begin, end, n);
 }
 
 void kv8_compact_launch(const Kv8Book& k, int most, int32_t* moves, hipStream_t stream) {
