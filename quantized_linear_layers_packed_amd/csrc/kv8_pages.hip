@@ -56,23 +56,30 @@ __device__ __forceinline__ int sum_before(int v, int* part, int* total) {
 
 // The pages of a step are dealt out 1024 to a wave, in 16 rows of 64: lane l's i-th is
 // first + 64 i + l, so that loads, and what is written for pages in turn, are
-// consecutive over the lanes.  Bit i: that page lies before `end` (which is above
-// 0) and is free.
-__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int at, int end) {
-  const int first = at + (threadIdx.x & ~63) * kEach + (threadIdx.x & 63);
+// consecutive over the lanes.  A row is a mask over the lanes, in scalar registers.
+struct Rows16 {
+  uint64_t row[kEach];
+  __device__ __forceinline__ int count() const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) n += __popcll(row[i]);
+    return n;
+  }
+};
+// Of the step's pages before `end` (which is above 0): which are free, or (USED) are not.
+template <bool USED = false>
+__device__ __forceinline__ Rows16 free_pages(const int32_t* refs, int at, int end) {
+  const int wave = __builtin_amdgcn_readfirstlane(at + (threadIdx.x & ~63) * kEach), first = wave + (threadIdx.x & 63);
+  Rows16 f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) f.row[i] = 0;
+  if (wave >= end) return f;
   int r[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) r[i] = refs[min(first + 64 * i, end - 1)];
-  uint32_t bits = 0;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) bits |= static_cast<uint32_t>(r[i] <= 0 && first + 64 * i < end) << i;
-  return bits;
-}
-__device__ __forceinline__ int wave_count(uint32_t bits) {
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) n += __popcll(__ballot((bits >> i) & 1u));
-  return n;
+  for (int i = 0; i < kEach; ++i) f.row[i] = __ballot((r[i] <= 0) != USED && first + 64 * i < end);
+  return f;
 }
 // Sum over the waves before this one of a number that is the same in all of a wave's
 // lanes, and over all waves in *total.
@@ -91,42 +98,46 @@ __device__ __forceinline__ int waves_before(int n, int* part, int* total) {
   __syncthreads();
   return before;
 }
-// give(rank, page) for the pages of a step that `bits` names, `rank` being that of the
-// wave's first, until `limit`.
+// give(rank, page) for the pages of a step, `rank` being that of the wave's first,
+// until `limit`.
 template <class Give>
-__device__ __forceinline__ void each_page(uint32_t bits, int at, int rank, int limit, Give give) {
+__device__ __forceinline__ void each_page(const Rows16& f, int at, int rank, int limit, Give give) {
   const int lane = threadIdx.x & 63, first = at + (threadIdx.x & ~63) * kEach + lane;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const uint64_t all = __ballot((bits >> i) & 1u);
-    const int mine = rank + __popcll(all & ((uint64_t{1} << lane) - 1));
-    if (((bits >> i) & 1u) && mine < limit) give(mine, first + 64 * i);
+    const uint64_t all = f.row[i];
+    if (all == 0) continue;
+    const int mine = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
+                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), static_cast<uint32_t>(rank)));
+    if (__builtin_amdgcn_inverse_ballot_w64(all) && mine < limit) give(mine, first + 64 * i);
     rank += __popcll(all);
   }
 }
 
 // give(rank, page) for the `wanted` lowest free pages in turn, if there are as many;
 // returns how many are missing (the same in every thread).  Nothing is given then.
-// ahead: free_bits of the first step, asked for before it was known how many pages
-// are wanted.
+// ahead: free_pages of the first step, asked for before it was known how many are
+// wanted.
 template <class Give>
-__device__ __forceinline__ int take_free(const int32_t* refs, int pages, int wanted, uint32_t ahead, int* part, Give give) {
+__device__ __forceinline__ int take_free(const int32_t* refs, int pages, int wanted, const Rows16& ahead, int* part, Give give) {
   int found = 0, steps = 0, before = 0;
   for (int at = 0; at < pages && found < wanted; at += kStep, ++steps) {
     int total;
-    before = found + waves_before(wave_count(at == 0 ? ahead : free_bits(refs, at, pages)), part, &total);
+    before = found + waves_before(at == 0 ? ahead.count() : free_pages(refs, at, pages).count(), part, &total);
     found += total;
   }
   if (found < wanted) return wanted - found;
   // every count has been read: what follows may change them
+  if (steps == 1) {
+    if (before < wanted) each_page(ahead, 0, before, wanted, give);
+    return 0;
+  }
   for (int s = 0, have = 0; s < steps; ++s) {
-    const uint32_t bits = s == 0 ? ahead : free_bits(refs, s * kStep, pages);
-    if (steps > 1) {
-      int total;
-      before = have + waves_before(wave_count(bits), part, &total);
-      have += total;
-    }
-    if (before < wanted) each_page(bits, s * kStep, before, wanted, give);
+    const Rows16 f = free_pages(refs, s * kStep, pages);
+    int total;
+    before = have + waves_before(f.count(), part, &total);
+    have += total;
+    if (before < wanted) each_page(f, s * kStep, before, wanted, give);
   }
   return 0;
 }
@@ -141,7 +152,7 @@ __device__ __forceinline__ int entries_of(int len, const Kv8Book& k) {
 // Pages for the entries behind each row's last held one, up to the row's tokens.
 // A row's need is known at once where its last entry, or the one before, is held (a
 // growing sequence); rows with more to find (prompts) are searched back from the end
-// by a wave each, 512 entries at a time.
+// by a wave each, 1024 entries at a time.
 __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, const int32_t* __restrict__ lens,
                                                             int2* __restrict__ moves) {
   extern __shared__ int start[];               // [rows + 1]: wanted pages before each row; before that the needs
@@ -150,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
   const int tid = threadIdx.x, lane = tid & 63;
   if (tid == 0) bad = searched = 0;
   __syncthreads();
-  const uint32_t ahead = free_bits(k.refs, 0, k.pages);
+  const Rows16 ahead = free_pages(k.refs, 0, k.pages);
   for (int b = tid; b < k.rows; b += kThreads) {
     const int want = entries_of(lens[b], k);
     const int32_t* row = k.table + static_cast<size_t>(b) * k.stride;
@@ -173,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
       if (start[b] >= 0) continue;             // (the wave's own rows: nobody else writes them)
       const int want = entries_of(lens[b], k);
       const int32_t* row = k.table + static_cast<size_t>(b) * k.stride;
-      constexpr int AHEAD = 8;
+      constexpr int AHEAD = 16;
       int last = -1;
       for (int end = want; end > 0 && last < 0; end -= 64 * AHEAD) {
         int page[AHEAD];
@@ -203,26 +214,88 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
   __syncthreads();
   // the row whose places hold a rank, start[row] <= rank < start[row + 1], and where its
   // entries end: a thread's ranks ascend, and often stay in the row
-  int row = -1, want = 0;
+  int row = -1, row_end = 0;
+  long long place = 0;                         // of rank 0 as the row would have it
   const int missing = total == 0 ? 0 : take_free(k.refs, k.pages, total, ahead, part, [&](int rank, int page) {
-    if (row < 0 || start[row + 1] <= rank) {
-      int lo = row < 0 ? 0 : row + 1, hi = k.rows;
+    if (rank >= row_end) {
+      int lo = row + 1, hi = k.rows;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= rank) lo = mid;
         else hi = mid;
       }
       row = lo;
-      want = entries_of(lens[row], k);
+      row_end = start[row + 1];
+      place = static_cast<long long>(row) * k.stride + entries_of(lens[row], k) - row_end;
     }
-    k.table[static_cast<size_t>(row) * k.stride + want - (start[row + 1] - rank)] = page;
+    k.table[place + rank] = page;
     k.refs[page] = 1;
   });
   if (tid == 0) moves[0] = make_int2(missing ? 0 : total, missing);
 }
 
+// Adds to the counts of pages, summed while the page stays the same: neighbours in a
+// list often share theirs (forks of one prefix: 64 children of 2 parents each way took
+// 8.6 us with an addition for every child).
+struct Counts {
+  int32_t* refs;
+  int page = -1, by = 0;
+  __device__ __forceinline__ void add(int p, int n) {
+    if (p != page) {
+      flush();
+      page = p;
+      by = 0;
+    }
+    by += n;
+  }
+  __device__ __forceinline__ void flush() {
+    if (page >= 0 && by != 0) atomicAdd(refs + page, by);
+  }
+};
+constexpr int kListEach = 8;                  // of a list, to a workgroup
+
+// Entries from e0 on, `step` apart, of the rows of children i0 .. i0 + 7: shared pages, the
+// fresh one, nothing behind; what they held before goes back.
+__device__ __forceinline__ void fork_rows(const Kv8Book& k, const int32_t* parents, const int32_t* children, const int32_t* lens,
+                                          int n, const int2* moves, int i0, int e0, int step) {
+  const int short_by = moves[0].y;
+  int p[kListEach], c[kListEach], len[kListEach], fresh[kListEach];
+#pragma unroll
+  for (int j = 0; j < kListEach; ++j) {
+    const int i = min(i0 + j, n - 1);
+    p[j] = parents[i];
+    c[j] = i0 + j < n ? children[i] : -1;
+    len[j] = lens[i];
+    fresh[j] = moves[1 + i].y;
+  }
+  if (short_by != 0) return;                   // (lists that do not fit the table among it)
+  for (int e = e0; e < k.stride; e += step) {
+    int was[kListEach], theirs[kListEach];
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j) {
+      was[j] = theirs[j] = -1;
+      if (p[j] < 0 || c[j] < 0) continue;      // padding
+      was[j] = k.table[static_cast<size_t>(c[j]) * k.stride + e];
+      if (e < len[j] >> k.log_page) theirs[j] = k.table[static_cast<size_t>(p[j]) * k.stride + e];
+    }
+    Counts more{k.refs}, fewer{k.refs};
+#pragma unroll
+    for (int j = 0; j < kListEach; ++j) {
+      if (p[j] < 0 || c[j] < 0) continue;
+      const int shared = is_page(theirs[j], k.pages) ? theirs[j] : -1, now = e == len[j] >> k.log_page ? fresh[j] : shared;
+      if (now == was[j]) continue;             // (never the fresh page: that one was free)
+      if (shared >= 0) more.add(shared, 1);
+      if (is_page(was[j], k.pages)) fewer.add(was[j], -1);
+      k.table[static_cast<size_t>(c[j]) * k.stride + e] = now;
+    }
+    more.flush();
+    fewer.flush();
+  }
+}
+
 // The plan of a fork: what is wrong with it, and a fresh page for each child whose
-// prefix ends inside a page.  n <= 16384 children.
+// prefix ends inside a page.  n <= 16384 children.  ROWS: the children's rows, too.
+template <bool ROWS>
 __global__ __launch_bounds__(kThreads) void kv8_fork_plan_kernel(const Kv8Book k, const int32_t* __restrict__ parents,
                                                                  const int32_t* __restrict__ children,
                                                                  const int32_t* __restrict__ lens, int n,
@@ -233,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_plan_kernel(const Kv8Book k
   const int tid = threadIdx.x, words = (k.rows + 31) / 32;
   int* is_child = held + n;
   int* is_parent = is_child + words;
-  const uint32_t ahead = free_bits(k.refs, 0, k.pages);
+  const Rows16 ahead = free_pages(k.refs, 0, k.pages);
   for (int i = tid; i < 2 * words; i += kThreads) is_child[i] = 0;
   if (tid == 0) bad = 0;
   __syncthreads();
@@ -276,68 +349,20 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_plan_kernel(const Kv8Book k
     moves[1 + i] = src >= 0 ? make_int2(src, held[rank++]) : make_int2(-1, -1);
   }
   if (tid == 0) moves[0] = make_int2(missing ? 0 : n, missing);
+  if constexpr (ROWS) {
+    __syncthreads();                           // every move is there, no fresh page is counted any more
+    const int groups = (n + kListEach - 1) / kListEach;
+    for (int at = tid; at < groups * k.stride; at += kThreads)
+      fork_rows(k, parents, children, lens, n, moves, at / k.stride * kListEach, at % k.stride, k.stride);
+  }
 }
 
-// Adds to the counts of pages, summed while the page stays the same: neighbours in a
-// list often share theirs (forks of one prefix: 64 children of 2 parents each way took
-// 8.6 us with an addition for every child).
-struct Counts {
-  int32_t* refs;
-  int page = -1, by = 0;
-  __device__ __forceinline__ void add(int p, int n) {
-    if (p != page) {
-      flush();
-      page = p;
-      by = 0;
-    }
-    by += n;
-  }
-  __device__ __forceinline__ void flush() {
-    if (page >= 0 && by != 0) atomicAdd(refs + page, by);
-  }
-};
-constexpr int kListEach = 8;                  // of a list, to a workgroup
-
-// The children's rows: shared pages, the fresh one, nothing behind; what they held
-// before goes back.  Grid: entries x children.
+// Grid: entries x children.
 __global__ __launch_bounds__(256) void kv8_fork_rows_kernel(const Kv8Book k, const int32_t* __restrict__ parents,
                                                             const int32_t* __restrict__ children,
                                                             const int32_t* __restrict__ lens, int n,
                                                             const int2* __restrict__ moves) {
-  const int i0 = blockIdx.y * kListEach;
-  const int short_by = moves[0].y;
-  int p[kListEach], c[kListEach], len[kListEach], fresh[kListEach];
-#pragma unroll
-  for (int j = 0; j < kListEach; ++j) {
-    const int i = min(i0 + j, n - 1);
-    p[j] = parents[i];
-    c[j] = i0 + j < n ? children[i] : -1;
-    len[j] = lens[i];
-    fresh[j] = moves[1 + i].y;
-  }
-  if (short_by != 0) return;                   // (lists that do not fit the table among it)
-  for (int e = blockIdx.x * 256 + threadIdx.x; e < k.stride; e += gridDim.x * 256) {
-    int was[kListEach], theirs[kListEach];
-#pragma unroll
-    for (int j = 0; j < kListEach; ++j) {
-      was[j] = theirs[j] = -1;
-      if (p[j] < 0 || c[j] < 0) continue;      // padding
-      was[j] = k.table[static_cast<size_t>(c[j]) * k.stride + e];
-      if (e < len[j] >> k.log_page) theirs[j] = k.table[static_cast<size_t>(p[j]) * k.stride + e];
-    }
-    Counts more{k.refs}, fewer{k.refs};
-#pragma unroll
-    for (int j = 0; j < kListEach; ++j) {
-      if (p[j] < 0 || c[j] < 0) continue;
-      const int shared = is_page(theirs[j], k.pages) ? theirs[j] : -1, now = e == len[j] >> k.log_page ? fresh[j] : shared;
-      if (now == was[j]) continue;             // (never the fresh page: that one was free)
-      if (shared >= 0) more.add(shared, 1);
-      if (is_page(was[j], k.pages)) fewer.add(was[j], -1);
-      k.table[static_cast<size_t>(c[j]) * k.stride + e] = now;
-    }
-    more.flush();
-    fewer.flush();
-  }
+  fork_rows(k, parents, children, lens, n, moves, blockIdx.y * kListEach, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 // Gives back the entries whose tokens all lie in begin .. end-1.  An entry is taken
@@ -376,61 +401,29 @@ __global__ __launch_bounds__(256) void kv8_free_kernel(const Kv8Book k, const in
   }
 }
 
-// The moves of a compaction: with U pages in use, every free page below U gets one of
-// the used pages from U on, the lowest the highest; at most `most` of them.
-__global__ __launch_bounds__(kThreads) void kv8_compact_plan_kernel(const Kv8Book k, int most, int2* __restrict__ moves) {
-  __shared__ int part[kThreads / 64];
-  const int tid = threadIdx.x;
-  int total, unused = 0;
-  for (int at = 0; at < k.pages; at += kStep) unused += wave_count(free_bits(k.refs, at, k.pages));
-  waves_before(unused, part, &total);
-  const int used = k.pages - total;
-  int low = 0;                                 // free pages below `used`: as many as there are used ones from there on
-  for (int at = 0; at < used; at += kStep) {
-    const uint32_t bits = free_bits(k.refs, at, used);
-    const int rank = low + waves_before(wave_count(bits), part, &total);
-    low += total;
-    each_page(bits, at, rank, most, [&](int r, int page) { moves[1 + r].y = page; });
-  }
-  for (int at = used, have = 0; at < k.pages && have < low; at += kStep) {
-    const uint32_t bits = free_bits(k.refs, at, k.pages);
-    uint32_t there = 0;                        // pages of the pool
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      there |= static_cast<uint32_t>(at + (tid & ~63) * kEach + 64 * i + (tid & 63) < k.pages) << i;
-    const int rank = have + waves_before(wave_count(there & ~bits), part, &total);
-    have += total;
-    each_page(there & ~bits, at, rank, low, [&](int r, int page) {
-      if (low - 1 - r < most) moves[1 + low - 1 - r].x = page;
-    });
-  }
-  const int count = min(low, most);
-  for (int i = count + tid; i < most; i += kThreads) moves[1 + i] = make_int2(-1, -1);
-  if (tid == 0) moves[0] = make_int2(count, 0);
-  __syncthreads();                             // every count has been read, every move is there
-  for (int i = tid; i < count; i += kThreads) {
-    const int2 m = moves[1 + i];
-    k.refs[m.y] = k.refs[m.x];
-    k.refs[m.x] = 0;
-  }
-}
-
-// The table after the moves: an entry from the lowest moved page on is looked up
-// among them (their sources descend), in a copy in LDS of all of them or of every
-// 2^s-th, and from there in the list itself.
+// The table after the moves: entries `step` apart are looked up among them (their
+// sources descend) where they are from the lowest moved page on, in a copy in LDS of
+// all of them or of every 2^s-th, and from there in the list itself.
 constexpr int kSamples = 4096;
-__global__ __launch_bounds__(256) void kv8_compact_rows_kernel(const Kv8Book k, const int2* __restrict__ moves) {
-  __shared__ int sample[kSamples];
+template <int NT>
+__device__ __forceinline__ void compact_rows(const Kv8Book& k, const int2* moves, int* sample, long long e0, long long step) {
   const int count = moves[0].x;
   if (count == 0) return;
   int shift = 0;
   while ((count - 1) >> shift >= kSamples) ++shift;
   const int samples = ((count - 1) >> shift) + 1;
-  for (int i = threadIdx.x; i < samples; i += 256) sample[i] = moves[1 + (i << shift)].x;
+  constexpr int AHEAD = 4;
+  for (int i = threadIdx.x; i < samples; i += AHEAD * NT) {
+    int x[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) x[j] = moves[1 + (min(i + j * NT, samples - 1) << shift)].x;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) sample[min(i + j * NT, samples - 1)] = x[j];
+  }
   const int lowest = moves[count].x;
   __syncthreads();
   const long long entries = static_cast<long long>(k.rows) * k.stride;
-  for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < entries; e += static_cast<long long>(gridDim.x) * 256) {
+  for (long long e = e0; e < entries; e += step) {
     const int page = k.table[e];
     if (page < lowest || !is_page(page, k.pages)) continue;
     int lo = 0, hi = samples - 1;              // the last of them whose source is at least the page
@@ -449,6 +442,51 @@ __global__ __launch_bounds__(256) void kv8_compact_rows_kernel(const Kv8Book k, 
     const int2 m = moves[1 + lo];
     if (m.x == page) k.table[e] = m.y;
   }
+}
+// The moves of a compaction: with U pages in use, every free page below U gets one of
+// the used pages from U on, the lowest the highest; at most `most` of them.
+// ROWS: the table, too.
+template <bool ROWS>
+__global__ __launch_bounds__(kThreads) void kv8_compact_plan_kernel(const Kv8Book k, int most, int2* __restrict__ moves) {
+  __shared__ int part[kThreads / 64];
+  const int tid = threadIdx.x;
+  int total, unused = 0;
+  for (int at = 0; at < k.pages; at += kStep) unused += free_pages(k.refs, at, k.pages).count();
+  waves_before(unused, part, &total);
+  const int used = k.pages - total;
+  int low = 0;                                 // free pages below `used`: as many as there are used ones from there on
+  for (int at = 0; at < used; at += kStep) {
+    const Rows16 f = free_pages(k.refs, at, used);
+    const int rank = low + waves_before(f.count(), part, &total);
+    low += total;
+    each_page(f, at, rank, most, [&](int r, int page) { moves[1 + r].y = page; });
+  }
+  for (int at = used, have = 0; at < k.pages && have < low; at += kStep) {
+    const Rows16 f = free_pages<true>(k.refs, at, k.pages);
+    const int rank = have + waves_before(f.count(), part, &total);
+    have += total;
+    each_page(f, at, rank, low, [&](int r, int page) {
+      if (low - 1 - r < most) moves[1 + low - 1 - r].x = page;
+    });
+  }
+  const int count = min(low, most);
+  for (int i = count + tid; i < most; i += kThreads) moves[1 + i] = make_int2(-1, -1);
+  if (tid == 0) moves[0] = make_int2(count, 0);
+  __syncthreads();                             // every count has been read, every move is there
+  for (int i = tid; i < count; i += kThreads) {
+    const int2 m = moves[1 + i];
+    k.refs[m.y] = k.refs[m.x];
+    k.refs[m.x] = 0;
+  }
+  if constexpr (ROWS) {
+    __shared__ int sample[kSamples];
+    compact_rows<kThreads>(k, moves, sample, tid, kThreads);
+  }
+}
+
+__global__ __launch_bounds__(256) void kv8_compact_rows_kernel(const Kv8Book k, const int2* __restrict__ moves) {
+  __shared__ int sample[kSamples];
+  compact_rows<256>(k, moves, sample, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, static_cast<long long>(gridDim.x) * 256);
 }
 
 // Pages listed in moves, of every layer: 16 bytes a lane, four loads in flight.
@@ -486,6 +524,10 @@ __global__ __launch_bounds__(256) void kv8_copy_kernel(const Kv8CopyArgs a) {
   }
 }
 
+// Up to so many table entries (of groups of children, of a whole table) the workgroup
+// that makes the plan writes them itself, which spares a launch.
+constexpr int kAlone = 1024;
+
 unsigned chunks_of(int n, int by, int most) { return static_cast<unsigned>(std::min((n + by - 1) / by, most)); }
 
 }  // namespace
@@ -499,7 +541,11 @@ void kv8_fork_launch(const Kv8Book& k, const int32_t* parents, const int32_t* ch
                      int32_t* moves, hipStream_t stream) {
   int2* m = reinterpret_cast<int2*>(moves);
   const size_t lds = sizeof(int) * (n + 2 * ((k.rows + 31) / 32));
-  hipLaunchKernelGGL(kv8_fork_plan_kernel, dim3(1), dim3(kThreads), lds, stream, k, parents, children, lens, n, m);
+  if (static_cast<int64_t>((n + kListEach - 1) / kListEach) * k.stride <= kAlone) {
+    hipLaunchKernelGGL(kv8_fork_plan_kernel<true>, dim3(1), dim3(kThreads), lds, stream, k, parents, children, lens, n, m);
+    return;
+  }
+  hipLaunchKernelGGL(kv8_fork_plan_kernel<false>, dim3(1), dim3(kThreads), lds, stream, k, parents, children, lens, n, m);
   hipLaunchKernelGGL(kv8_fork_rows_kernel, dim3(chunks_of(k.stride, 256, 64), chunks_of(n, kListEach, n)), dim3(256), 0, stream,
                      k, parents, children, lens, n, static_cast<const int2*>(m));
 }
@@ -511,8 +557,12 @@ void kv8_free_launch(const Kv8Book& k, const int32_t* rows, const int32_t* begin
 
 void kv8_compact_launch(const Kv8Book& k, int most, int32_t* moves, hipStream_t stream) {
   int2* m = reinterpret_cast<int2*>(moves);
-  hipLaunchKernelGGL(kv8_compact_plan_kernel, dim3(1), dim3(kThreads), 0, stream, k, most, m);
   const long long entries = static_cast<long long>(k.rows) * k.stride;
+  if (entries <= kAlone) {
+    hipLaunchKernelGGL(kv8_compact_plan_kernel<true>, dim3(1), dim3(kThreads), 0, stream, k, most, m);
+    return;
+  }
+  hipLaunchKernelGGL(kv8_compact_plan_kernel<false>, dim3(1), dim3(kThreads), 0, stream, k, most, m);
   hipLaunchKernelGGL(kv8_compact_rows_kernel, dim3(static_cast<unsigned>(std::min<long long>((entries + 255) / 256, 4096))),
                      dim3(256), 0, stream, k, static_cast<const int2*>(m));
 }

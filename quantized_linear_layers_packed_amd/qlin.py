@@ -587,7 +587,7 @@ class Kv8Caches:
 
 def _list(name, t, count):
     """Pointer of an int32 tensor [count]."""
-    if tuple(t.shape) != (count,):
+    if t.shape != (count,):
         raise ValueError(f"{name}: [{count}] expected, got shape {tuple(t.shape)}")
     _typed(name, t, _INDICES)
     return _ptr(t)
