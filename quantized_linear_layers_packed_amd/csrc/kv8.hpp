@@ -149,7 +149,9 @@ Kv8AttnPlan kv8_attn_plan(const Kv8AttnArgs& a);
 // With the workspace's counters and the memory after them.
 void kv8_attn_launch(Kv8AttnPlan p, int* counters, char* partials, int dtype, hipStream_t stream);
 // The kernel for many rows: rows of a workgroup, workgroups that share a compute
-// unit, bytes of a split's partial result.
+// unit, bytes of a split's partial result; and for documents, where row tiles are not
+// split, waves of a workgroup (of 32 rows each).
+int kv8_prompt_document_waves(int dim);
 int kv8_prompt_rows(int dim);
 int kv8_prompt_resident(int dim);
 size_t kv8_prompt_partial(int dim);

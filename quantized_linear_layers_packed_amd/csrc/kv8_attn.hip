@@ -437,7 +437,7 @@ int rows_waves(const Kv8AttnArgs& a, int nt, long long units, long long tiles, i
 
 // The launch of one kernel for sequences of up to `rows` rows (nt as above): its
 // grid and splits; returns the bytes of its partial results.
-size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
+size_t plan_splits(Kv8AttnArgs* a, int nt, long long rows, int cus) {
   a->row_columns = nt;
   const long long tile_rows = nt ? 16 * nt : kv8_prompt_rows(a->c.dim);
   const long long most = std::min(std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads)), 65535LL);
@@ -478,6 +478,20 @@ size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
   if (a->splits == 1) return 0;
   const size_t partial = nt ? static_cast<size_t>(tile_rows) * (a->c.dim + 2) * sizeof(float) : kv8_prompt_partial(a->c.dim);
   return static_cast<size_t>(units) * splits * partial;
+}
+
+// The same; for documents, row tiles of the kernel for many rows that are not split are
+// smaller ones, which need no workspace either.
+size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
+  const size_t bytes = plan_splits(a, nt, rows, cus);
+  const int waves = kv8_prompt_document_waves(a->c.dim);
+  if (!nt && a->starts && a->splits == 1 && 32 * waves < kv8_prompt_rows(a->c.dim)) {
+    const long long most = std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads));
+    a->waves = waves;
+    a->row_tiles = static_cast<int>(std::min(std::min((rows + 32 * waves - 1) / (32 * waves), most), 65535LL));
+    a->by_row_tiles = FastDiv(a->row_tiles);
+  }
+  return bytes;
 }
 
 void few_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {

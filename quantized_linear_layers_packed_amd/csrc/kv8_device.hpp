@@ -141,6 +141,15 @@ __device__ __forceinline__ uint32_t sight_bits(int j0, int start, int last, int 
   return held ? seen : 0u;
 }
 
+// The same of a whole tile from position j0.
+__device__ __forceinline__ uint64_t sight_tile(int j0, int start, int last, int low, int kept) {
+  const auto below = [&](int end) {
+    const int n = min(max(end - j0, 0), 64);
+    return n == 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
+  };
+  return below(last + 1) & ~below(start) & (~below(low) | below(kept));
+}
+
 // cap tanh(x / cap) in the exponent of two, plus `add`: cap - 2 cap / (e^(2 x / cap) + 1),
 // with z = 2 log2(e) x / cap and cap times log2(e).  Its error stays below 2^-21 cap: with
 // caps of up to 1024 less than 2^-11 of a weight.  Infinite x give +-cap.
