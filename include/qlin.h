@@ -452,7 +452,7 @@ qlin_status qlin_kv8_attention(const qlin_kv8_cache* cache, const qlin_kv8_batch
 /* Other scores and masks.  With x = scale q.k and the query at position p, in this
  * order:
  *   cap > 0        x becomes cap tanh(x / cap); cap from 2^-10 to 2^10, 0: none
- *   slopes         x -= slopes[query head] * |p - j|; NULL: none
+ *   slopes         x -= slopes[query head] * |p - j|, finite; NULL: none
  *   prefix_lens    positions j < prefix_lens[b] of sequence b are visible to its queries
  *                  at earlier positions too (a prefix read in both directions; queries
  *                  behind it see it anyway); NULL: none
@@ -470,7 +470,7 @@ typedef struct {
 
 /* qlin_kv8_attention with these scores and masks; all else, the workspace among it, as
  * there.  A capped score is within 2^-21 cap of the formula's; infinite ones are cap or
- * -cap.  2 log2(e) scale / cap has to be finite.  Positions up to 2^24 apart are exact in
+ * -cap.  2 log2(e) scale / cap has to be finite, also times a key scale.  Positions up to 2^24 apart are exact in
  * the bias, which is added in fp32.  Tiles that no row of a tile of queries sees are not
  * read: packed documents cost what they see, not the square of their sum. */
 qlin_status qlin_kv8_attention_scored(const qlin_kv8_cache* cache, const qlin_kv8_batch* batch,
@@ -506,9 +506,10 @@ typedef struct {
 
 /* Pages for longer sequences: in each row b, the entries behind its last held one
  * below ceil(lens[b] / page_size), up to that one, get a page each (entries before
- * it, given back behind a sliding window, stay empty).  lens device int32 [rows];
- * rows of lengths up to 0 get nothing, a length past the table's end is refused
- * (short -1).  moves int32 [1][2]: the pages taken, and short. */
+ * it, given back behind a sliding window, stay empty; a row that holds none gets all
+ * of them).  lens device int32 [rows]; rows of lengths up to 0 get nothing, a length
+ * past the table's end is refused (short -1).  moves int32 [1][2]: the pages taken, and
+ * short; nothing is to be copied. */
 qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_t* moves, hipStream_t stream);
 
 /* Sequences that go on from the first lens[i] tokens of another: row children[i]
@@ -519,8 +520,10 @@ qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_
  * Lists: device int32 [count], count <= 16384; a negative parent or child marks an
  * entry of padding.  Refused (short -1, nothing done): rows past the table, lengths
  * below 0 or past the table, a child named twice or as a parent.
- * A sequence that is cut back into a page that it shares must not be appended to:
- * fork its prefix to another row instead.  moves int32 [1 + count][2]. */
+ * A prefix must not be longer than its parent is: pages that it would share are still
+ * being filled.  A sequence that is cut back into a page that it shares must not be
+ * appended to: fork its prefix to another row instead.  moves int32 [1 + count][2],
+ * all written, a pair for each child. */
 qlin_status qlin_kv8_fork(const qlin_kv8_book* book, const int32_t* parents, const int32_t* children, const int32_t* lens,
                           int count, int32_t* moves, hipStream_t stream);
 

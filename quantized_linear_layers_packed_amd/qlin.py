@@ -602,8 +602,11 @@ def _moves(t, least=0):
 
 
 def qlin_kv8_grow(book, lens, moves, stream=None):
-    """lens int32 [rows]; moves int32 [1][2] (or longer, of which the first pair is written)."""
-    _check(_lib.qlin_kv8_grow(book.ref, _list("lens", lens, book.rows), _moves(moves)[0], _stream(stream)))
+    """lens int32 [rows]; moves int32 [1][2]: the pages taken, and how many were short."""
+    p, pairs = _moves(moves)
+    if pairs:
+        raise ValueError(f"moves: [1][2] expected, got shape {tuple(moves.shape)}")
+    _check(_lib.qlin_kv8_grow(book.ref, _list("lens", lens, book.rows), p, _stream(stream)))
 
 
 def qlin_kv8_fork(book, parents, children, lens, moves, stream=None):

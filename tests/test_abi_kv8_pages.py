@@ -79,7 +79,7 @@ def test_binding_checks_shapes_and_types():
     k, v, s = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2, 64, 16, dtype=torch.int8), torch.zeros(4, 2, 2)
     c = qlin.Kv8Cache(k, v, s)
     for call in (lambda: qlin.qlin_kv8_grow(b, i(4), i(1, 2), stream=0), lambda: qlin.qlin_kv8_grow(b, i(3), i(2), stream=0),
-                 lambda: qlin.qlin_kv8_grow(b, i(3).long(), i(1, 2), stream=0), lambda: qlin.qlin_kv8_grow(b, i(3), i(0, 2), stream=0),
+                 lambda: qlin.qlin_kv8_grow(b, i(3).long(), i(1, 2), stream=0), lambda: qlin.qlin_kv8_grow(b, i(3), i(0, 2), stream=0), lambda: qlin.qlin_kv8_grow(b, i(3), i(5, 2), stream=0),
                  lambda: qlin.qlin_kv8_fork(b, i(2), i(3), i(2), i(3, 2), stream=0),
                  lambda: qlin.qlin_kv8_fork(b, i(2), i(2), i(2), i(2, 2), stream=0),
                  lambda: qlin.qlin_kv8_free(b, i(2), i(1), stream=0), lambda: qlin.qlin_kv8_free(b, i(2), None, i(2).float(), stream=0),
