@@ -41,6 +41,11 @@
 // and 4 us of the 49 us of 131072 tokens).  Tried without gain: 32 positions to a step
 // with twice the waves (64 sequences 103 -> 117 us at the time), 128 registers for
 // four waves per SIMD (103 -> 141).
+//
+// SCORED: capped scores, a bias by distance, sights with a start and a prefix
+// (Kv8Sight).  The cache's bytes still bound it: 64 ragged sequences in a window of
+// 4096 (383 MB, capped) 77 us, 4.9 TB/s, one of 32768 with 32 heads of their own
+// (269 MB, biased) 48 us, 5.6 TB/s; a short chat takes what it takes without.
 
 #include <algorithm>
 

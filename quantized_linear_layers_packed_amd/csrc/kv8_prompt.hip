@@ -22,6 +22,19 @@
 // each.  Tried without gain: the next tile's scores beside this tile's weights
 // (30 more registers; 7 % for heads of 256 only, since overtaken by the look-ahead),
 // vector work dealt out between the products by hand, 4 waves instead of 8.
+//
+// With other scores (cap tanh(x / cap) as cap - 2 cap / (e^(2 x / cap) + 1), a bias of a
+// slope times the distance, sights that begin and end where starts and prefixes say)
+// a score takes two transcendental instructions and three others more, or two for
+// the bias.  The prompt of 8192 then takes 1440 us with a cap (760 TFLOP/s), 1270 with a
+// bias, 1155 with neither: vector units busy 69 % of the cycles and matrix units
+// 32 %, one after the other: a SIMD's two waves fill its vector unit only together
+// (two at once run an instruction in 2.7 cycles, one alone in 5.3; transcendental
+// ones 9.6 and 12).  Tried without gain: the reference folded into the scores' addend
+// (one instruction of a score less: 1440 -> 1475 us), one half of a tile's products
+// dealt out between the other half's scores (1475, heads of 256 490 -> 610), the two
+// waves of a SIMD in opposite phases (1440 -> 1680), priorities of waves,
+// the longest sequences first (ragged prompts of heads of 256 490 -> 506).
 
 #include <algorithm>
 
