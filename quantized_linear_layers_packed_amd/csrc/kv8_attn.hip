@@ -63,37 +63,6 @@ namespace {
 constexpr int row_occupancy(int dim, int nt) { return dim * nt <= 128 ? 2 : 1; }
 constexpr int kMostSplits = 64;           // a lane each when they are joined
 constexpr int kMostManySplits = 256;      // of the kernel for many rows: joined by a kernel of its own
-// 16 NT query rows as B operands: lane (q, g), slice (u, e) holds dimensions
-// 64 u + 16 g + 8 e .. + 7 of row q.  bf16 rows are scaled by a power of two into
-// fp16's range; *mul is what undoes it.
-template <int D, bool BF16>
-__device__ __forceinline__ void load_rows(const uint16_t* row, int g, h8_t (&q)[D / 64][2], float* mul) {
-  uint4 w[D / 64][2];
-#pragma unroll
-  for (int u = 0; u < D / 64; ++u)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) w[u][e] = *reinterpret_cast<const uint4*>(row + 64 * u + 16 * g + 8 * e);
-  if constexpr (!BF16) {
-    *mul = 1.0f;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) q[u][e] = bitcast<h8_t>(w[u][e]);
-  } else {
-    uint32_t most = 0;
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) most = max(most, chunk_most(w[u][e]));
-    const int e14 = row_exponent(most_over_g(most));
-    *mul = ldexpf(1.0f, e14);
-#pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) q[u][e] = chunk_f16(w[u][e], e14);
-  }
-}
-
 // Partial result of a split: [16 NT][D] sums, then [16 NT] (reference, sum of weights).
 template <int D, int NT>
 constexpr size_t kPartial = 16 * NT * (D + 2);

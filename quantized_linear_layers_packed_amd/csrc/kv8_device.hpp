@@ -226,6 +226,37 @@ __device__ __forceinline__ h8_t chunk_f16(const uint4& w, int e) {
   return q;
 }
 
+// 16 query rows as B operands of the 16x16x32 products: lane (q, g), slice (u, e) holds dimensions
+// 64 u + 16 g + 8 e .. + 7 of row q.  bf16 rows are scaled by a power of two into
+// fp16's range; *mul is what undoes it.
+template <int D, bool BF16>
+__device__ __forceinline__ void load_rows(const uint16_t* row, int g, h8_t (&q)[D / 64][2], float* mul) {
+  uint4 w[D / 64][2];
+#pragma unroll
+  for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) w[u][e] = *reinterpret_cast<const uint4*>(row + 64 * u + 16 * g + 8 * e);
+  if constexpr (!BF16) {
+    *mul = 1.0f;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) q[u][e] = bitcast<h8_t>(w[u][e]);
+  } else {
+    uint32_t most = 0;
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) most = max(most, chunk_most(w[u][e]));
+    const int e14 = row_exponent(most_over_g(most));
+    *mul = ldexpf(1.0f, e14);
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) q[u][e] = chunk_f16(w[u][e], e14);
+  }
+}
+
 // What sums of weighted codes are multiplied by, from the sum of weights and the
 // row's reference: rows that see nothing give zeros, rows that see scores of -inf
 // alone NaN.

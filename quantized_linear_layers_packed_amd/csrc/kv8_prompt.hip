@@ -98,6 +98,8 @@ constexpr int kPlain = 0, kScored = 1, kCapped = 2;
 // documents of 745 tokens on average 141 -> 133 us.  Prompts without documents are as
 // fast with 8 or up to 2 % faster.
 constexpr int kDocumentWaves = 4;
+// Waves of a workgroup of the kernel with 16 rows to a wave.
+constexpr int kThinWaves = 8;
 
 // A row tile: rows r0 .. r0 + nrows - 1 of a sequence, the tiles they see and how
 // many of them a split takes.  Row tiles beyond those planned for are not split:
@@ -422,6 +424,197 @@ __global__ __launch_bounds__(64 * W, kPromptOccupancy<D>) void kv8_prompt_kernel
   }
 }
 
+// The same for whole row tiles of wide heads with other scores, on the 16x16x32
+// instruction: a wave holds 16 rows, so that two of them share a SIMD, whose vector
+// unit a single wave fills half.  S^T and P lie as in the kernel for few rows
+// (kv8_attn.hip): lane (q, g) gets the weights of row q and the run of tokens 16 g ..
+// 16 g + 15, and one pair of scales.  K's rows lie in LDS in the order in which the
+// products take them (row 16 t + r: token 16 (r / 4) + 4 t + r % 4).
+template <int D, bool BF16, bool CAP>
+__global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8AttnArgs a) {
+  constexpr int W = kThinWaves, NT = 64 * W, ROWS = 16 * W, DT = D / 16, KU = D / 64;
+  constexpr int NL = D * kTile / 16 / NT;                  // 16-byte pieces of K (and of V) per thread and tile
+  extern __shared__ __align__(16) char smem[];
+  Tile16<D>* tile = reinterpret_cast<Tile16<D>*>(smem);    // two of them
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, ql = lane & 15;
+  const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
+  const int b = a.by_row_tiles(unit);
+  const Kv8Seq seq = kv8_seq(a.c, b);
+  const int P = 1 << a.c.log_page, G = a.group;
+  const int rows = seq.count * G;                             // below 2^30
+  if (rows < a.least_rows || rows > a.most_rows) return;
+  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.table_stride;
+  const int last_entry = (seq.len - 1) >> a.c.log_page;    // entries past it are not read
+  for (int r0 = (a.row_tiles - 1 - (unit - b * a.row_tiles)) * ROWS; r0 < rows; r0 += a.row_tiles * ROWS) {
+    const RowTile<D, kScored, W / 2> rt(a, seq, b, rows, r0);
+    const int nrows = rt.nrows, p0 = rt.p0;
+    const Kv8Tiles& tiles = rt.tiles;
+    const int count = tiles.count;
+
+    // this lane's row
+    const int r = r0 + min(16 * wv + ql, nrows - 1), t = a.by_group(r), hq = head * G + r - t * G;
+    const int pos = seq.start + t;
+    const int low_most = a.window > 0 ? max(rt.p1, 0) - a.window + 1 : 0;
+    const int start = a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0;
+    const float slope = a.slopes ? a.slopes[hq] * -1.44269504088896340736f : 0.0f;
+    h8_t qf[KU][2];
+    float cq;
+    load_rows<D, BF16>(a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(hq) * D, g, qf, &cq);
+    cq *= a.scale;
+    f32x4_t o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = kNone, l = 0.0f;
+
+    // Loads of a tile, as above.
+    constexpr int STEP = NT / (D / 16);
+    const size_t block_bytes = static_cast<size_t>(D) << a.c.log_page;
+    const int token = tid / (D / 16);
+    const uint32_t kplace = (token & (P - 1)) * D + 16 * (tid % (D / 16));
+    const uint32_t vplace = ((tid / 4) << a.c.log_page) + ((16 * (tid % 4)) & (P - 1));
+    const int kentry = token >> a.c.log_page, ventry = (16 * (tid % 4)) >> a.c.log_page;
+    uint4 kw[NL], vw[NL];
+    int kpage[NL], vpage;
+    float2 scale2;
+    bool held_next;
+    auto block_of = [&](int page) {                         // pages that are not there: any other
+      return static_cast<uint32_t>(static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages) ? page : 0) * a.c.heads + head;
+    };
+    auto load_pages = [&](int x) {
+      const int entry = (tiles[min(x, count - 1)] * kTile) >> a.c.log_page;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) kpage[n] = table[static_cast<unsigned>(min(entry + kentry + ((n * STEP) >> a.c.log_page), last_entry))];
+      vpage = table[static_cast<unsigned>(min(entry + ventry, last_entry))];
+    };
+    auto load_codes = [&](int x) {
+      const int within = (tiles[min(x, count - 1)] * kTile) & (P - 1);
+#pragma unroll
+      for (int n = 0; n < NL; ++n)
+        kw[n] = *reinterpret_cast<const uint4*>(a.c.k + (block_of(kpage[n]) * block_bytes + (kplace + (within + ((n * STEP) & (P - 1))) * D)));
+      const uint32_t block = block_of(vpage);
+#pragma unroll
+      for (int n = 0; n < NL; ++n)
+        vw[n] = *reinterpret_cast<const uint4*>(a.c.v + (block * block_bytes + (vplace + within + ((n * (NT / 4)) << a.c.log_page))));
+      scale2 = reinterpret_cast<const float2*>(a.c.scales)[block];
+      held_next = static_cast<unsigned>(vpage) < static_cast<unsigned>(a.c.pages);
+    };
+    auto put_codes = [&](Tile16<D>& to) __attribute__((always_inline)) {
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        const int i = tid + n * NT, token = i / (D / 16), c = i % (D / 16);
+        _Float16* k = to.k[4 * (token & 12) + 4 * (token >> 4) + (token & 3)] + 16 * c;
+        *reinterpret_cast<h8_t*>(k) = codes_f16(kw[n].x, kw[n].y);
+        *reinterpret_cast<h8_t*>(k + 8) = codes_f16(kw[n].z, kw[n].w);
+        *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4)]) = codes_f16(vw[n].x, vw[n].y);
+        *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4) + 8]) = codes_f16(vw[n].z, vw[n].w);
+      }
+    };
+    auto put_runs = [&](Tile16<D>& to) {
+      if (tid < 4) {
+        const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
+        to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs)};
+      }
+      const uint32_t held = static_cast<uint32_t>(__ballot(held_next)) & 15u;  // lanes 0 .. 3 of wave 0: the four runs
+      if (tid == 0) to.held = held;
+    };
+
+    if (count > 0) {
+      load_pages(0);
+      load_codes(0);
+      load_pages(1);
+      put_codes(tile[0]);
+      put_runs(tile[0]);
+      for (int x = 0; x < count; ++x) {
+        const Tile16<D>& now = tile[x & 1];
+        const int base = tiles[x] * kTile;
+        load_codes(x + 1);
+        load_pages(x + 2);
+        __syncthreads();                                      // the tile is complete, and the other one is free
+        f32x4_t st[4];
+#pragma unroll
+        for (int T = 0; T < 4; ++T) st[T] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int T = 0; T < 4; ++T)
+              st[T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8_t*>(&now.k[16 * T + ql][64 * u + 16 * g + 8 * e]),
+                                                             qf[u][e], st[T], 0, 0, 0);
+        lookahead<8 * KU>();
+        const Run run = now.run[g];
+        const uint32_t held = __builtin_amdgcn_readfirstlane(now.held);
+        const float c = run.key * cq;
+        const bool full = base + kTile - 1 <= rt.sight.last(p0) && base >= rt.sight.start1 &&
+                          (base >= low_most || base + kTile <= rt.sight.kept0) && held == 15u;
+        float iv = run.iv, top = kLowest;
+#pragma unroll
+        for (int T = 0; T < 4; ++T)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st[T][i] = CAP ? capped(st[T][i] * c, a.cap, run.lv) : fmaf(st[T][i], c, run.lv);
+        if (a.slopes) {
+          const float away = static_cast<float>(base + 16 * g - pos);
+#pragma unroll
+          for (int T = 0; T < 4; ++T)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[T][i] = fmaf(slope, fabsf(away + static_cast<float>(4 * T + i)), st[T][i]);
+        }
+        if (!full) {
+          const uint32_t seen = sight_bits<16>(base + 16 * g, start, rt.sight.last(pos), a.window > 0 ? max(pos, 0) - a.window + 1 : 0,
+                                               start + min(a.sinks, seq.len - start), (held >> g) & 1u);
+          iv = seen != 0 ? iv : 0.0f;                         // scales of hidden pages may be anything, NaN among it
+#pragma unroll
+          for (int T = 0; T < 4; ++T)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[T][i] = (seen >> (4 * T + i)) & 1u ? st[T][i] : -INFINITY;
+          top = seen != 0 ? kLowest : kNone;
+        }
+#pragma unroll
+        for (int T = 0; T < 4; ++T)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, st[T][i]);
+        if (__any(top > m + kSlack)) {
+          const float high = max_over_g(top), was = m;
+          m = high > was + kSlack ? high - kHead : was;               // by the row's own scores alone
+          const float f = __builtin_amdgcn_exp2f(was - m);
+          l *= f;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[d] *= f;
+        }
+        h8_t pf[2];
+        float part = 0.0f;
+#pragma unroll
+        for (int T = 0; T < 4; ++T)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = __builtin_amdgcn_exp2f(st[T][i] - m);     // hidden: exp2(-inf) = 0
+            part += p;
+            pf[T >> 1][4 * (T & 1) + i] = static_cast<_Float16>(p);
+          }
+        l = fmaf(part, iv, l);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8_t*>(&now.v[16 * d + ql][16 * g + 8 * e]), pf[e], o[d],
+                                                          0, 0, 0);
+        put_codes(tile[(x + 1) & 1]);
+        lookahead<2 * DT>();
+        put_runs(tile[(x + 1) & 1]);
+      }
+    }
+    const float inv = by_weights(sum_over_g(l), m);
+    if (16 * wv + ql < nrows) {
+      uint16_t* y = a.Y + (static_cast<size_t>(seq.row + t) * a.q_heads + hq) * D + 4 * g;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        *reinterpret_cast<uint2*>(y + 16 * d) = make_uint2(pack2<BF16>(o[d][0] * inv, o[d][1] * inv), pack2<BF16>(o[d][2] * inv, o[d][3] * inv));
+    }
+    __syncthreads();                                        // the tiles may be used for the next rows
+  }
+}
+
 // Joins the splits of row tiles, in their order, spread over the whole device (one
 // workgroup joining 64 splits of 256 rows would read 9 MB by itself): a row tile's
 // wave and a group of four of its sums are a task, of SHARE waves that take
@@ -514,8 +707,23 @@ void form_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
 }
 
 template <int D>
+void thin_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.c.seqs) * a.row_tiles * a.c.heads), block(64 * kThinWaves);
+  const bool bf16 = dtype == QLIN_BF16;
+  const auto fn = a.cap > 0.0f ? (bf16 ? kv8_thin_kernel<D, true, true> : kv8_thin_kernel<D, false, true>)
+                               : (bf16 ? kv8_thin_kernel<D, true, false> : kv8_thin_kernel<D, false, false>);
+  hipLaunchKernelGGL(fn, grid, block, 2 * sizeof(Tile16<D>), stream, a);
+}
+
+template <int D>
 void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   constexpr int W = kPromptWaves<D>;
+  if constexpr (D == 256) {
+    if (a.scored && a.splits == 1) {
+      thin_launch<D>(a, dtype, stream);
+      return;
+    }
+  }
   if (!a.scored) form_launch<D, kPlain, W>(a, dtype, stream);
   else if (W != kDocumentWaves && a.waves == kDocumentWaves)
     a.cap > 0.0f ? form_launch<D, kCapped, kDocumentWaves>(a, dtype, stream) : form_launch<D, kScored, kDocumentWaves>(a, dtype, stream);

@@ -342,3 +342,102 @@ def test_graph_replays_with_other_lengths_documents_and_slopes():
         ref = okv.attention_scored(s.k, s.v, s.scales, s.offsets, s.kv_lens, s.table, back(q), 0.125, 0, 0, 30.0,
                                    slopes.cpu().numpy(), [0, 0], starts.cpu().numpy())
         assert (np.abs(got - ref[0]) <= scored_bound(*(ref[k] for k in (1, 0, 2, 3, 4)), 64, 600, F16, 30.0)).all()
+
+
+# Row tiles that are not split over the cache (planned for short sequences, so that small batches are not either): the
+# kernels for whole prompts, of which heads of 256 and documents have their own.
+WHOLE = [
+    (F16, 256, 32, 1, 2, [130, 20], [190, 400]), (BF16, 256, 16, 2, 3, [90, 33, 1], [200, 33, 70]),
+    (BF16, 256, 128, 1, 8, [65, 17], [300, 17]), (F16, 256, 64, 1, 1, [400], [650]),
+    (F16, 128, 64, 1, 8, [90, 40], [300, 64]), (BF16, 128, 16, 2, 4, [129, 31], [129, 500]), (F16, 64, 32, 1, 4, [200, 70], [260, 70]),
+]
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("dtype,D,P,Hk,G,new,kv", WHOLE)
+def test_whole_row_tiles_within_their_rounding_bounds(dtype, D, P, Hk, G, new, kv, form):
+    say(f"kv8 scored attention, whole row tiles, {form}: D={D} P={P} Hk={Hk} G={G} new={new} kv={kv}")
+    s = Setup(51, D, P, Hk, new, kv, max_kv=64)
+    kw = dict(FORMS[form])
+    if "slopes" in kw:
+        kw["slopes"] = alibi(Hk * G)
+    if "prefix" in kw:
+        kw["prefix"] = [[m - n // 3, m, 0][b % 3] for b, (n, m) in enumerate(zip(new, kv))]
+    if "starts" in kw:
+        kw["starts"] = documents(s, kw["starts"])
+    kw["Q"] = (12.0 if kw.get("cap") else 3.0) * s.rng.standard_normal((s.T, Hk * G, D))
+    first = back(check_scored(s, G, dtype, **kw))
+    assert np.array_equal(back(run_scored(s, G, dtype, **kw)[0]), first)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_whole_row_tiles_at_the_edges_of_sight(D):
+    """Nothing in sight, tokens before the first position, a sequence without pages, garbage for starts and prefixes; pages
+    out of sight that hold anything or nothing; queries that are not finite stay in their rows."""
+    torch = torch_cuda()
+    s = Setup(52, D, 16, 2, [60, 63, 0, 2, 60], [100, 60, 30, 40, 300], max_kv=64)
+    s.table[3, :] = -1
+    s.upload()
+    o = s.offsets
+    starts = np.zeros(s.T, np.int32)
+    starts[o[0]:o[1]] = np.arange(40, 100) + 1
+    starts[o[4]:o[5]:2] = 1 << 30
+    starts[o[4] + 1:o[5]:2] = 130
+    Q = 3.0 * s.rng.standard_normal((s.T, 8, D))
+    for prefix in (None, [-5, -(1 << 31), 1 << 30, 3, 0]):
+        Y = back(check_scored(s, 4, F16, Q=Q, starts=starts, prefix=prefix, slopes=alibi(8), cap=20.0))
+        assert not Y[o[0]:o[1]].any() and not Y[o[1]:o[1] + 3].any() and not Y[o[3]:o[4]].any() and not Y[o[4]:o[5]:2].any()
+        check_scored(s, 4, BF16, Q=Q, starts=starts, prefix=prefix, window=30, sinks=7)
+    clean = back(run_scored(s, 4, F16, Q=Q, starts=starts, cap=20.0)[0])
+    for i, garbage in enumerate((np.nan, np.inf, -np.inf, -1.0)):
+        s.scales[s.table[4, i]] = garbage                                    # positions below 64, all before 130
+    s.table[4, 4:8] = -1
+    s.upload()
+    assert np.array_equal(back(run_scored(s, 4, F16, Q=Q, starts=starts, cap=20.0)[0]), clean)
+    Q[o[4] + 1, 3, 5], Q[o[4] + 3, 1, 0] = np.nan, np.inf
+    Y = back(run_scored(s, 4, F16, Q=Q, starts=starts, slopes=alibi(8))[0])
+    Z = back(run_scored(s, 4, F16, Q=np.nan_to_num(Q, nan=1.0, posinf=1.0), starts=starts, slopes=alibi(8))[0])
+    bad = np.zeros(Y.shape[:2], bool)
+    bad[o[4] + 1, 3] = bad[o[4] + 3, 1] = True
+    assert np.isnan(Y[bad]).all() and np.array_equal(Y[~bad], Z[~bad])
+
+
+def test_two_streams_at_once():
+    """Books, copies and attention of two serving programs side by side, each with its own buffers."""
+    torch = torch_cuda()
+    made = []
+    for seed in (61, 62):
+        r = np.random.default_rng(seed)
+        s = Setup(seed, 128, 16, 2, [1, 40, 1], [900, 300, 77])
+        b = Book(500, 8, 40)
+        b.deal(r, [30, 17, 0, 0, 0, 0, 0, 0])
+        q, _ = to16(3.0 * r.standard_normal((s.T, 8, 128)), F16)
+        need = qlin.qlin_kv8_attention_workspace_bytes(s.cache, s.batch, 8)
+        made.append(dict(s=s, b=b, q=q, y=torch.empty_like(q), ws=torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda"),
+                         how=qlin.Kv8Scoring(25.0, up(alibi(8), F), up([0, 290, 0]), up(documents(s, 50))), moves=b.moves(3),
+                         lists=[up([0, 1, 0]), up([2, 3, 4]), up([470, 100, 33])], lens=up([480, 300, 480, 0, 40, 0, 0, 5]), grown=b.moves(0),
+                         stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def step(m, stream):
+        parents, kids, lens = m["lists"]
+        for _ in range(3):
+            qlin.qlin_kv8_free(m["b"].book, kids, stream=stream)
+            qlin.qlin_kv8_fork(m["b"].book, parents, kids, lens, m["moves"], stream=stream)
+            qlin.qlin_kv8_grow(m["b"].book, m["lens"], m["grown"], stream=stream)
+            qlin.qlin_kv8_attention_scored(m["s"].cache, m["s"].batch, m["q"], F16, 8, 0.1, 0, 0, m["how"], m["y"], m["ws"], stream=stream)
+
+    def result(m):
+        return [x.clone() for x in (m["b"].d_table, m["b"].d_refs, m["moves"], m["grown"], m["y"])]
+
+    for _ in range(4):
+        for m in made:
+            step(m, m["stream"])
+    torch.cuda.synchronize()
+    both = [result(m) for m in made]
+    for m, got in zip(made, both):
+        step(m, None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(result(m)[2:3] + result(m)[4:], got[2:3] + got[4:]))
+        table, refs = m["b"].d_table.cpu().numpy(), m["b"].d_refs.cpu().numpy()
+        assert np.array_equal(np.bincount(table[table >= 0], minlength=500), refs) and int(m["grown"][0, 1]) == 0
