@@ -424,18 +424,37 @@ __global__ __launch_bounds__(64 * W, kPromptOccupancy<D>) void kv8_prompt_kernel
   }
 }
 
-// The same for whole row tiles of wide heads with other scores, on the 16x16x32
+// The same for whole row tiles of heads of 256 with other scores, on the 16x16x32
 // instruction: a wave holds 16 rows, so that two of them share a SIMD, whose vector
-// unit a single wave fills half.  S^T and P lie as in the kernel for few rows
-// (kv8_attn.hip): lane (q, g) gets the weights of row q and the run of tokens 16 g ..
-// 16 g + 15, and one pair of scales.  K's rows lie in LDS in the order in which the
-// products take them (row 16 t + r: token 16 (r / 4) + 4 t + r % 4).
+// unit a single wave fills half: ragged prefix prompts 488 -> 354 us.  S^T and P lie as in
+// the kernel for few rows (kv8_attn.hip): lane (q, g) gets the weights of row q and the
+// run of tokens 16 g .. 16 g + 15, and one pair of scales.  K's rows lie in LDS in the
+// order in which the products take them (row 16 t + r: token 16 (r / 4) + 4 t + r % 4).
+//
+// Every wave reads all of a tile, so LDS has to deliver 64 KB for 1024 cycles of a wave's
+// products.  The 16 bytes of lane (r, g) of an operand lie in a plane for each g, a
+// multiple of all the banks apart, and swizzled by r so that 16 rows fill every bank
+// once, whichever g's the lanes that are served together belong to; a g's own constants
+// keep the planes' swizzles apart for the writes: 354 -> 317 us (padded rows: a third of
+// the time bank conflicts).  What is left is vector (62 % of the cycles) and matrix
+// instructions (32 %).  Heads of 128 this way, four waves to a SIMD, are slower than with
+// 32 rows to a wave (a capped prompt of 8192 1449 -> 1678 us).
+template <int D>
+struct alignas(16) ThinTile {
+  h8_t k[4][kTile][D / 32];                                 // [g][row][slice (u, e) ^ thin_k(row, g)]
+  h8_t v[4][D][2];                                          // [g][dimension ^ thin_v(g)][e ^ bit 3 of that]
+  Run run[4];
+  uint32_t held;                                            // bit s: run s has a page
+};
+__device__ __forceinline__ int thin_k(int row, int g) { return ((row >> 1) & 7) ^ ((0x7610 >> (4 * g)) & 7); }
+__device__ __forceinline__ int thin_v(int g) { return (g & 1) ? 12 : 0; }
+
 template <int D, bool BF16, bool CAP>
 __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8AttnArgs a) {
   constexpr int W = kThinWaves, NT = 64 * W, ROWS = 16 * W, DT = D / 16, KU = D / 64;
   constexpr int NL = D * kTile / 16 / NT;                  // 16-byte pieces of K (and of V) per thread and tile
   extern __shared__ __align__(16) char smem[];
-  Tile16<D>* tile = reinterpret_cast<Tile16<D>*>(smem);    // two of them
+  ThinTile<D>* tile = reinterpret_cast<ThinTile<D>*>(smem);    // two of them
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, ql = lane & 15;
   const int unit = a.by_heads(blockIdx.x), head = blockIdx.x - unit * a.c.heads;
   const int b = a.by_row_tiles(unit);
@@ -498,18 +517,20 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
       scale2 = reinterpret_cast<const float2*>(a.c.scales)[block];
       held_next = static_cast<unsigned>(vpage) < static_cast<unsigned>(a.c.pages);
     };
-    auto put_codes = [&](Tile16<D>& to) __attribute__((always_inline)) {
+    auto put_codes = [&](ThinTile<D>& to) __attribute__((always_inline)) {
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         const int i = tid + n * NT, token = i / (D / 16), c = i % (D / 16);
-        _Float16* k = to.k[4 * (token & 12) + 4 * (token >> 4) + (token & 3)] + 16 * c;
-        *reinterpret_cast<h8_t*>(k) = codes_f16(kw[n].x, kw[n].y);
-        *reinterpret_cast<h8_t*>(k + 8) = codes_f16(kw[n].z, kw[n].w);
-        *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4)]) = codes_f16(vw[n].x, vw[n].y);
-        *reinterpret_cast<h8_t*>(&to.v[i / 4][16 * (i % 4) + 8]) = codes_f16(vw[n].z, vw[n].w);
+        const int row = 4 * (token & 12) + 4 * (token >> 4) + (token & 3), swizzle = thin_k(row, c % 4);
+        h8_t* k = to.k[c % 4][row];
+        k[(2 * (c / 4)) ^ swizzle] = codes_f16(kw[n].x, kw[n].y);
+        k[(2 * (c / 4) + 1) ^ swizzle] = codes_f16(kw[n].z, kw[n].w);
+        const int d = (i / 4) ^ thin_v(i % 4), first = (d >> 3) & 1;
+        to.v[i % 4][d][first] = codes_f16(vw[n].x, vw[n].y);
+        to.v[i % 4][d][first ^ 1] = codes_f16(vw[n].z, vw[n].w);
       }
     };
-    auto put_runs = [&](Tile16<D>& to) {
+    auto put_runs = [&](ThinTile<D>& to) {
       if (tid < 4) {
         const float vs = scale2.y < kLeastScale ? kLeastScale : scale2.y;     // NaN stays
         to.run[tid] = Run{scale2.x, __log2f(vs), __builtin_amdgcn_rcpf(vs)};
@@ -518,6 +539,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
       if (tid == 0) to.held = held;
     };
 
+    const int k_swizzle = thin_k(ql, g), v_row = ql ^ thin_v(g);
     if (count > 0) {
       load_pages(0);
       load_codes(0);
@@ -525,7 +547,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
       put_codes(tile[0]);
       put_runs(tile[0]);
       for (int x = 0; x < count; ++x) {
-        const Tile16<D>& now = tile[x & 1];
+        const ThinTile<D>& now = tile[x & 1];
         const int base = tiles[x] * kTile;
         load_codes(x + 1);
         load_pages(x + 2);
@@ -539,7 +561,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int T = 0; T < 4; ++T)
-              st[T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8_t*>(&now.k[16 * T + ql][64 * u + 16 * g + 8 * e]),
+              st[T] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.k[g][16 * T + ql][(2 * u + e) ^ k_swizzle],
                                                              qf[u][e], st[T], 0, 0, 0);
         lookahead<8 * KU>();
         const Run run = now.run[g];
@@ -597,7 +619,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int d = 0; d < DT; ++d)
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8_t*>(&now.v[16 * d + ql][16 * g + 8 * e]), pf[e], o[d],
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(now.v[g][16 * d + v_row][e ^ (v_row >> 3)], pf[e], o[d],
                                                           0, 0, 0);
         put_codes(tile[(x + 1) & 1]);
         lookahead<2 * DT>();
@@ -712,7 +734,7 @@ void thin_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
   const bool bf16 = dtype == QLIN_BF16;
   const auto fn = a.cap > 0.0f ? (bf16 ? kv8_thin_kernel<D, true, true> : kv8_thin_kernel<D, false, true>)
                                : (bf16 ? kv8_thin_kernel<D, true, false> : kv8_thin_kernel<D, false, false>);
-  hipLaunchKernelGGL(fn, grid, block, 2 * sizeof(Tile16<D>), stream, a);
+  hipLaunchKernelGGL(fn, grid, block, 2 * sizeof(ThinTile<D>), stream, a);
 }
 
 template <int D>
