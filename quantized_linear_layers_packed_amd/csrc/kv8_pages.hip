@@ -17,7 +17,7 @@
 // Measured, calls and all: a token for each of 256 sequences (131072 pages; two
 // releases and the grow) 15.6 us, of which the host's three calls are 14; 32768 pages
 // for 16 prompts 28.5 us (the grow 23: one workgroup's 65536 stores, and the search for
-// the rows' ends); 128 forks of two prompts with a page of 131 KB each to copy in 4 layers
+// the rows' ends), 16168 for 512 prompts of 32 pages 58; 128 forks of two prompts with a page of 131 KB each to copy in 4 layers
 // 39 us, the copies 17; a pool of 6082 pages half in use, 1520 of 262 KB moved in 2 layers,
 // 168 us, 4.75 TB/s (a large copy: 4.74).
 
@@ -156,16 +156,59 @@ __device__ __forceinline__ int entries_of(int len, const Kv8Book& k) {
   return n <= k.stride ? n : -1;
 }
 
+// Needs of the rows that have more to find: searched back from the end for the last
+// held entry, ROWS rows of a wave and 1024 / ROWS entries of each at a time.  With one, few
+// long rows are found soonest (16 of 2500 entries: 4 reads in turn), with four, many short
+// ones (512 of 47 entries: TIMES).
+constexpr int kAFew = 2 * kThreads / 64;
+template <int ROWS>
+__device__ __forceinline__ void search_rows(const Kv8Book& k, const int32_t* lens, int* need) {
+  constexpr int AHEAD = 16 / ROWS;
+  const int lane = threadIdx.x & 63;
+  for (int b = (threadIdx.x >> 6) * ROWS; b < k.rows; b += kThreads / 64 * ROWS) {
+    int want[ROWS], end[ROWS], last[ROWS];
+    bool more = false;
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {           // (the wave's own rows: nobody else writes them)
+      want[j] = end[j] = b + j < k.rows && need[b + j] < 0 ? entries_of(lens[b + j], k) : 0;
+      last[j] = -1;
+      more |= end[j] > 0;
+    }
+    while (more) {
+      int page[ROWS][AHEAD];
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          page[j][i] = k.table[static_cast<size_t>(min(b + j, k.rows - 1)) * k.stride + max(end[j] - 1 - 64 * i - lane, 0)];
+      more = false;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const uint64_t held = __ballot(end[j] - 1 - 64 * i - lane >= 0 && is_page(page[j][i], k.pages));
+          if (held != 0 && last[j] < 0) last[j] = end[j] - 1 - 64 * i - (__ffsll(static_cast<unsigned long long>(held)) - 1);
+        }
+        end[j] = last[j] >= 0 ? 0 : end[j] - 64 * AHEAD;
+        more |= end[j] > 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j)
+      if (lane == 0 && want[j] > 0) need[b + j] = want[j] - 1 - last[j];
+  }
+}
+
 // Pages for the entries behind each row's last held one, up to the row's tokens.
-// A row's need is known at once where its last entry, or the one before, is held (a
-// growing sequence); rows with more to find (prompts) are searched back from the end
-// by a wave each, 1024 entries at a time.
+// A row's need is known at once where one of its last four entries is held (a growing
+// sequence) or it has no more; rows with more to find (prompts) are searched.
+constexpr int kLook = 4;
 __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, const int32_t* __restrict__ lens,
                                                             int2* __restrict__ moves) {
   extern __shared__ int start[];               // [rows + 1]: wanted pages before each row; before that the needs
   __shared__ int part[kThreads / 64];
   __shared__ int bad, searched;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   if (tid == 0) bad = searched = 0;
   __syncthreads();
   const Rows16 ahead = free_pages(k.refs, 0, k.pages);
@@ -175,10 +218,14 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
     int need = 0;
     if (want < 0) bad = 1;
     if (want > 0) {
-      const int last = row[want - 1], before = row[max(want - 2, 0)];
-      need = is_page(last, k.pages) ? 0 : want == 1 || is_page(before, k.pages) ? 1 : -1;
+      int page[kLook];
+#pragma unroll
+      for (int i = 0; i < kLook; ++i) page[i] = row[max(want - 1 - i, 0)];
+      need = want <= kLook ? want : -1;        // unless one of them is held
+#pragma unroll
+      for (int i = kLook - 1; i >= 0; --i) need = want > i && is_page(page[i], k.pages) ? i : need;
     }
-    if (need < 0) searched = 1;
+    if (need < 0) atomicAdd(&searched, 1);
     start[b] = need;
   }
   __syncthreads();
@@ -186,27 +233,9 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
     if (tid == 0) moves[0] = make_int2(0, -1);
     return;
   }
-  if (searched) {
-    for (int b = tid >> 6; b < k.rows; b += kThreads / 64) {
-      if (start[b] >= 0) continue;             // (the wave's own rows: nobody else writes them)
-      const int want = entries_of(lens[b], k);
-      const int32_t* row = k.table + static_cast<size_t>(b) * k.stride;
-      constexpr int AHEAD = 16;
-      int last = -1;
-      for (int end = want; end > 0 && last < 0; end -= 64 * AHEAD) {
-        int page[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) page[i] = row[max(end - 1 - 64 * i - lane, 0)];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          const uint64_t held = __ballot(end - 1 - 64 * i - lane >= 0 && is_page(page[i], k.pages));
-          if (held != 0 && last < 0) last = end - 1 - 64 * i - (__ffsll(static_cast<unsigned long long>(held)) - 1);
-        }
-      }
-      if (lane == 0) start[b] = want - 1 - last;
-    }
-    __syncthreads();
-  }
+  if (searched > kAFew) search_rows<4>(k, lens, start);
+  else if (searched > 0) search_rows<1>(k, lens, start);
+  if (searched > 0) __syncthreads();
   // needs to places, in runs of consecutive rows to a thread
   const int per = (k.rows + kThreads - 1) / kThreads, b0 = min(tid * per, k.rows), b1 = min(b0 + per, k.rows);
   int mine = 0, total;

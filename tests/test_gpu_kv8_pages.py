@@ -139,6 +139,28 @@ def test_long_rows_are_searched_back_from_the_end():
     assert b.grow([16 * 2100 - 5] * 12 + [0, 16 * 2100] + [16 * 2100] * 5 + [16 * 1589 + 1])[1] == 0
 
 
+@pytest.mark.parametrize("per_row", [200, 600])
+@pytest.mark.parametrize("rows", [31, 32, 33, 71, 600])
+def test_many_rows_with_much_to_find(rows, per_row):
+    """Rows of every kind side by side: nothing held, a few entries, holes before the last held one, nothing wanted; lengths
+    around the number of entries that are looked at first, and at the borders of the search's steps.  The smaller pool
+    does not hold all that is wanted."""
+    r = np.random.default_rng(rows)
+    b = Book(per_row * rows, rows, 1100)
+    held = r.choice([0, 0, 1, 2, 3, 4, 5, 60, 64, 65, 255, 256, 257, 300], rows)
+    b.deal(r, held)
+    for row in range(0, rows, 3):
+        b.table[row, :max(held[row] - 2, 0)] = -1
+    b.refs[:] = np.bincount(b.table[b.table >= 0], minlength=len(b.refs))
+    b.upload()
+    for more in ([0, 1, 2, 3, 4, 5, 6], [0, 100, 256, 255, 257], [1, 3, 4, 5]):
+        want = np.minimum(held + r.choice(more, rows), 1100)
+        lens = want * 16 - r.integers(0, 16, rows)
+        lens[r.uniform(size=rows) < 0.1] = r.choice([0, -5, 1])
+        assert b.grow(lens)[1] == 0 or per_row == 200
+        held = np.array([max([e + 1 for e in range(1100) if b.table[row, e] >= 0], default=0) for row in range(rows)])
+
+
 def test_many_rows_and_forks():
     r = np.random.default_rng(9)
     b = Book(60000, 32767, 3)
