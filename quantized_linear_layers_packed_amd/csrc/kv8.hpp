@@ -90,7 +90,7 @@ struct Kv8AttnArgs {
   int least_rows, most_rows;   // of a sequence that this launch computes
   // the split of long sequences (see kv8_attn.hip)
   int row_columns, row_tiles, splits, chunk, waves;
-  bool sorted;          // sequences in the order of their lengths
+  bool sorted;          // few rows: sequences in the order of their lengths; many: a sequence's row tiles in that of theirs
   FastDiv by_group, by_heads, by_row_tiles, by_splits;
   int* counters;
   float* partials;

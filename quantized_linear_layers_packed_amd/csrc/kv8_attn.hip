@@ -455,7 +455,7 @@ size_t plan_splits(Kv8AttnArgs* a, int nt, long long rows, int cus) {
 }
 
 // The same; for documents, row tiles of the kernel for many rows that are not split are
-// smaller ones, which need no workspace either.
+// smaller ones, which need no workspace either, and those with the most tiles begin first.
 size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
   const size_t bytes = plan_splits(a, nt, rows, cus);
   const int waves = kv8_prompt_document_waves(a->c.dim);
@@ -465,6 +465,8 @@ size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
     a->row_tiles = static_cast<int>(std::min(std::min((rows + 32 * waves - 1) / (32 * waves), most), 65535LL));
     a->by_row_tiles = FastDiv(a->row_tiles);
   }
+  if (!nt && a->starts && a->splits == 1)
+    a->sorted = a->row_tiles > 1 && static_cast<long long>(a->c.seqs) * a->row_tiles * a->c.heads > cus;
   return bytes;
 }
 

@@ -402,6 +402,22 @@ def test_whole_row_tiles_at_the_edges_of_sight(D):
     assert np.isnan(Y[bad]).all() and np.array_equal(Y[~bad], Z[~bad])
 
 
+@pytest.mark.parametrize("dtype,D,G,Hk,new,kv", [
+    (F16, 128, 8, 4, [1070, 30], [1070, 90]),              # 67 row tiles: 33 pairs and one
+    (BF16, 256, 8, 3, [1050, 0, 1], [1111, 5, 300]), (F16, 64, 4, 8, [600, 599, 1, 90], [600, 700, 40, 90]),
+    (BF16, 128, 2, 30, [129, 700], [640, 700]),            # fewer than 64
+])
+def test_long_documents_first(dtype, D, G, Hk, new, kv):
+    """Enough row tiles that those with the most tiles are begun with: each is computed once, whatever the starts say."""
+    s = Setup(53, D, 16, Hk, new, kv, max_kv=64)
+    r = np.random.default_rng(54)
+    Q = 3.0 * r.standard_normal((s.T, Hk * G, D))
+    wild = r.integers(-100, max(kv) + 100, s.T).astype(np.int32)           # rising and falling from token to token
+    for kw in (dict(starts=documents(s, 333), slopes=alibi(Hk * G)), dict(starts=wild, prefix=[m // 2 for m in kv], window=200, sinks=9)):
+        first = back(check_scored(s, G, dtype, Q=Q, **kw))
+        assert np.array_equal(back(run_scored(s, G, dtype, Q=Q, **kw)[0]), first)
+
+
 def test_two_streams_at_once():
     """Books, copies and attention of two serving programs side by side, each with its own buffers."""
     torch = torch_cuda()
