@@ -484,8 +484,8 @@ qlin_status qlin_kv8_attention_scored(const qlin_kv8_cache* cache, const qlin_kv
 /* A book on the device says which pages of a pool are in use: refs[p] is the
  * number of block table entries that hold page p (0: free).  Rows of its table
  * are sequences (a qlin_kv8_batch may use the same table), entries outside
- * 0 .. num_pages-1 hold nothing; the calls write -1 there.  A new book has zeros
- * and -1 everywhere.  Any number of caches (the layers of a model) may share a book;
+ * 0 .. num_pages-1 hold nothing; the calls write -1 there, or -2 where a fork's prefix
+ * ends in a page that is gone (below).  A new book has zeros and -1 everywhere.  Any number of caches (the layers of a model) may share a book;
  * the calls below change the book alone and say in `moves` which pages are to be
  * copied in each of them, which qlin_kv8_copy_pages then does.
  * Choices depend on the book alone: free pages are taken from the lowest on, in
@@ -504,10 +504,10 @@ typedef struct {
   int num_pages, page_size, rows, table_stride;
 } qlin_kv8_book;
 
-/* Pages for longer sequences: in each row b, the entries behind its last held one
- * below ceil(lens[b] / page_size), up to that one, get a page each (entries before
- * it, given back behind a sliding window, stay empty; a row that holds none gets all
- * of them).  lens device int32 [rows]; rows of lengths up to 0 get nothing, a length
+/* Pages for longer sequences: in each row b, the entries behind its last held one (or
+ * its last -2) below ceil(lens[b] / page_size), up to that one, get a page each (entries
+ * before it, given back behind a sliding window, stay empty; a row that has neither is a
+ * new one and gets all of them).  lens device int32 [rows]; rows of lengths up to 0 get nothing, a length
  * past the table's end is refused (short -1).  moves int32 [1][2]: the pages taken, and
  * short; nothing is to be copied. */
 qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_t* moves, hipStream_t stream);
@@ -520,6 +520,10 @@ qlin_status qlin_kv8_grow(const qlin_kv8_book* book, const int32_t* lens, int32_
  * Lists: device int32 [count], count <= 16384; a negative parent or child marks an
  * entry of padding.  Refused (short -1, nothing done): rows past the table, lengths
  * below 0 or past the table, a child named twice or as a parent.
+ * Entries that the parent does not hold are empty in the child too.  If the prefix's last
+ * one is among them, it becomes -2: its tokens are cached and gone, grow gives pages behind
+ * it alone, and tokens appended to the rest of that page are not stored.  So let a prefix
+ * end in a page that its parent holds, or at that page's end.
  * A prefix must not be longer than its parent is: pages that it would share are still
  * being filled.  A sequence that is cut back into a page that it shares must not be
  * appended to: fork its prefix to another row instead.  moves int32 [1 + count][2],

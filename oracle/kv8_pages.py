@@ -1,5 +1,5 @@
 """The book of the 8-bit cache's pages: refs int32 [pages] (table entries that hold each page), table int32
-[rows][entries], -1 for none.  Every call updates both in place and returns the pairs of `moves`, the first
+[rows][entries], -1 for none, GONE where a fork's prefix ends in a page that its parent had given back.  Every call updates both in place and returns the pairs of `moves`, the first
 (count, short) among them.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
@@ -7,6 +7,8 @@ TEST INFRASTRUCTURE ONLY (see the package docstring).
 from __future__ import annotations
 
 import numpy as np
+
+GONE = -2
 
 
 def _free(refs):
@@ -27,7 +29,7 @@ def grow(refs, table, page_size, lens):
         return [(0, -1)]
     places = []
     for b, w in enumerate(want):
-        held = [e for e in range(w) if _is_page(table[b, e], refs)]
+        held = [e for e in range(w) if _is_page(table[b, e], refs) or table[b, e] == GONE]
         places += [(b, e) for e in range(held[-1] + 1 if held else 0, w)]
     free = _free(refs)
     if len(places) > len(free):
@@ -67,6 +69,9 @@ def fork(refs, table, page_size, parents, children, lens):
                 refs[p] += 1
         if moves[i][1] >= 0:
             row[full] = moves[i][1]
+        last = _entries(lens[i], page_size) - 1
+        if last >= 0 and row[last] < 0:
+            row[last] = GONE
         table[children[i]] = row
     return [(len(parents), 0)] + moves
 

@@ -109,6 +109,9 @@ struct Kv8Book {
   int pages, log_page, rows, stride;
 };
 
+// A table entry of tokens that a forked row counts but whose page its parent had given back.
+constexpr int kKv8Gone = -2;
+
 // Copies of listed pages, layer by layer.
 constexpr int kCopyLayers = 32;           // of a launch
 struct Kv8CopyLayer {

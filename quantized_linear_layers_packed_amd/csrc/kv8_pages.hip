@@ -36,6 +36,9 @@ constexpr int kEach = 16;                     // pages of a thread in a step
 constexpr int kStep = kThreads * kEach;
 
 __device__ __forceinline__ bool is_page(int page, int pages) { return static_cast<unsigned>(page) < static_cast<unsigned>(pages); }
+// An entry that grow looks for pages behind: held, or its tokens came with a fork and their
+// page was gone by then.  Pages dealt out for such tokens would show what others left there.
+__device__ __forceinline__ bool is_past(int page, int pages) { return is_page(page, pages) || page == kKv8Gone; }
 
 // Sum of v over the threads before this one, and over all in *total.
 // part: 16 ints in LDS, free again when the call returns.
@@ -157,7 +160,7 @@ __device__ __forceinline__ int entries_of(int len, const Kv8Book& k) {
 }
 
 // Needs of the rows that have more to find: searched back from the end for the last
-// held entry, ROWS rows of a wave and 1024 / ROWS entries of each at a time.  With one, few
+// held (or gone) entry, ROWS rows of a wave and 1024 / ROWS entries of each at a time.  With one, few
 // long rows are found soonest (16 of 2500 entries: 4 reads in turn), with four, many short
 // ones (512 prompts of 32 pages 89 -> 58 us).
 constexpr int kAFew = 2 * kThreads / 64;
@@ -186,7 +189,7 @@ __device__ __forceinline__ void search_rows(const Kv8Book& k, const int32_t* len
       for (int j = 0; j < ROWS; ++j) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-          const uint64_t held = __ballot(end[j] - 1 - 64 * i - lane >= 0 && is_page(page[j][i], k.pages));
+          const uint64_t held = __ballot(end[j] - 1 - 64 * i - lane >= 0 && is_past(page[j][i], k.pages));
           if (held != 0 && last[j] < 0) last[j] = end[j] - 1 - 64 * i - (__ffsll(static_cast<unsigned long long>(held)) - 1);
         }
         end[j] = last[j] >= 0 ? 0 : end[j] - 64 * AHEAD;
@@ -199,7 +202,7 @@ __device__ __forceinline__ void search_rows(const Kv8Book& k, const int32_t* len
   }
 }
 
-// Pages for the entries behind each row's last held one, up to the row's tokens.
+// Pages for the entries behind each row's last held (or gone) one, up to the row's tokens.
 // A row's need is known at once where one of its last four entries is held (a growing
 // sequence) or it has no more; rows with more to find (prompts) are searched.
 constexpr int kLook = 4;
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void kv8_grow_kernel(const Kv8Book k, con
       for (int i = 0; i < kLook; ++i) page[i] = row[max(want - 1 - i, 0)];
       need = want <= kLook ? want : -1;        // unless one of them is held
 #pragma unroll
-      for (int i = kLook - 1; i >= 0; --i) need = want > i && is_page(page[i], k.pages) ? i : need;
+      for (int i = kLook - 1; i >= 0; --i) need = want > i && is_past(page[i], k.pages) ? i : need;
     }
     if (need < 0) atomicAdd(&searched, 1);
     start[b] = need;
@@ -291,7 +294,8 @@ struct Counts {
 constexpr int kListEach = 8;                  // of a list, to a workgroup
 
 // Entries from e0 on, `step` apart, of the rows of children i0 .. i0 + 7: shared pages, the
-// fresh one, nothing behind; what they held before goes back.
+// fresh one, nothing behind; what they held before goes back.  The prefix's last entry says
+// so if the parent's page is gone: else the row would look like one with tokens to come.
 __device__ __forceinline__ void fork_rows(const Kv8Book& k, const int32_t* parents, const int32_t* children, const int32_t* lens,
                                           int n, const int2* moves, int i0, int e0, int step) {
   const int short_by = moves[0].y;
@@ -318,7 +322,9 @@ __device__ __forceinline__ void fork_rows(const Kv8Book& k, const int32_t* paren
 #pragma unroll
     for (int j = 0; j < kListEach; ++j) {
       if (p[j] < 0 || c[j] < 0) continue;
-      const int shared = is_page(theirs[j], k.pages) ? theirs[j] : -1, now = e == len[j] >> k.log_page ? fresh[j] : shared;
+      const int shared = is_page(theirs[j], k.pages) ? theirs[j] : -1;
+      int now = e == len[j] >> k.log_page ? fresh[j] : shared;
+      if (now < 0 && e == (len[j] - 1) >> k.log_page) now = kKv8Gone;
       if (now == was[j]) continue;             // (never the fresh page: that one was free)
       if (shared >= 0) more.add(shared, 1);
       if (is_page(was[j], k.pages)) fewer.add(was[j], -1);

@@ -296,3 +296,48 @@ def test_a_captured_step_replays_on_the_book_as_it_stands():
         for x, y in zip((b.d_refs, b.d_table, *t, *moves), (*twin, m_fork, m_grow, m_compact)):
             assert torch.equal(x, y)
         assert int(moves[1][0, 1]) == 0 and int(moves[0][0, 1]) == 0
+
+
+@pytest.mark.parametrize("rows,prefix", [(3, 700), (80, 40), (80, 700)])
+def test_pages_that_a_fork_never_had_are_not_dealt_out(rows, prefix):
+    """Prefixes that end in pages their parent gave back, grown by a token, by pages, and far; few rows and many, which are
+    searched in different ways, and where the mark is among the entries that are looked at first."""
+    b = Book(200 * rows, rows, 100)
+    b.deal(np.random.default_rng(rows), [60] + [0] * (rows - 1))
+    b.free([0], [0], [900])
+    kids = np.arange(1, rows)
+    lens = np.concatenate([[0], prefix + np.arange(rows - 1) % 33])
+    assert b.fork([0] * len(kids), kids, lens[1:]) == (len(kids), 0)
+    last = (lens[1:] - 1) // 16
+    assert (b.table[kids, last] == pages.GONE).all()
+    for more in (0, 1, 40, 700):
+        assert b.grow(np.where(lens > 0, lens + more, 0))[1] == 0
+        assert (b.table[kids, last] == pages.GONE).all() and all((b.table[k, :e] == -1).all() for k, e in zip(kids, last))
+    b.compact(100)
+    b.free([1])
+    assert b.grow([0, 16 * 50] + [0] * (rows - 2)) == (50, 0)
+
+
+def test_tokens_of_a_fork_whose_pages_are_gone_stay_hidden():
+    """Book, append and attention together: a child whose prefix its parent had given back sees its own new tokens and
+    nothing of what lies in the pool's pages."""
+    torch = torch_cuda()
+    P, D, H = 16, 64, 1
+    b = Book(30, 2, 8, P)
+    [t] = layers(np.random.default_rng(2), 1, 30, H, P, D)
+    t[2].fill_(float("nan"))                                       # what others left: whoever sees it gets NaN
+    cache = qlin.Kv8Cache(*t)
+    b.grow([100, 0])
+    b.free([0], [0], [48])
+    b.fork([0], [1], [40])
+    b.grow([0, 50])                                                # tokens 40 .. 47 have no page, 48 and 49 have
+    x = torch.ones((10, 3 * H, D), dtype=torch.float16, device="cuda")
+    y = torch.empty((10, H, D), dtype=torch.float16, device="cuda")
+    batch = qlin.Kv8Batch(up([0, 0, 10]), up([100, 50]), b.d_table, 10, 10, 50)
+    qlin.qlin_kv8_append(cache, batch, None, x[:, H:2 * H], x[:, 2 * H:], qlin.QLIN_F16, H, None, None, 0, qlin.QLIN_ROPE_HALF, None)
+    need = qlin.qlin_kv8_attention_workspace_bytes(cache, batch, H)
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    qlin.qlin_kv8_attention_scored(cache, batch, x[:, :H], qlin.QLIN_F16, H, 0.125, 0, 0, qlin.Kv8Scoring(20.0), y, ws)
+    torch.cuda.synchronize()
+    assert not y[:8].any()                                         # they see nothing, themselves among it
+    assert torch.equal(y[8:], x[8:, :H])                           # ones, in codes of 127 and a scale of 1 / 127
