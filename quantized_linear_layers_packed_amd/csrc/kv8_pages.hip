@@ -297,7 +297,7 @@ constexpr int kListEach = 8;                  // of a list, to a workgroup
 // fresh one, nothing behind; what they held before goes back.  The prefix's last entry says
 // so if the parent's page is gone: else the row would look like one with tokens to come.
 __device__ __forceinline__ void fork_rows(const Kv8Book& k, const int32_t* parents, const int32_t* children, const int32_t* lens,
-                                          int n, const int2* moves, int i0, int e0, int step) {
+                                          int n, const int2* moves, int i0, unsigned e0, unsigned step) {
   const int short_by = moves[0].y;
   int p[kListEach], c[kListEach], len[kListEach], fresh[kListEach];
 #pragma unroll
@@ -309,7 +309,8 @@ __device__ __forceinline__ void fork_rows(const Kv8Book& k, const int32_t* paren
     fresh[j] = moves[1 + i].y;
   }
   if (short_by != 0) return;                   // (lists that do not fit the table among it)
-  for (int e = e0; e < k.stride; e += step) {
+  for (unsigned at = e0; at < static_cast<unsigned>(k.stride); at += step) {   // (past the end it may leave int's range)
+    const int e = static_cast<int>(at);
     int was[kListEach], theirs[kListEach];
 #pragma unroll
     for (int j = 0; j < kListEach; ++j) {
@@ -427,7 +428,8 @@ __global__ __launch_bounds__(256) void kv8_free_kernel(const Kv8Book k, const in
     first = min(first, e0[j]);
     last = max(last, e1[j]);
   }
-  for (int e = first + blockIdx.x * 256 + threadIdx.x; e < last; e += gridDim.x * 256) {
+  for (unsigned at = first + blockIdx.x * 256 + threadIdx.x; at < static_cast<unsigned>(last); at += gridDim.x * 256) {
+    const int e = static_cast<int>(at);        // (past the end `at` may leave int's range)
     int was[kListEach];
 #pragma unroll
     for (int j = 0; j < kListEach; ++j)
@@ -570,7 +572,8 @@ __global__ __launch_bounds__(256) void kv8_copy_kernel(const Kv8CopyArgs a) {
 // that makes the plan writes them itself, which spares a launch.
 constexpr int kAlone = 1024;
 
-unsigned chunks_of(int n, int by, int most) { return static_cast<unsigned>(std::min((n + by - 1) / by, most)); }
+constexpr unsigned chunks_of(int64_t n, int by, int most) { return static_cast<unsigned>(std::min<int64_t>((n + by - 1) / by, most)); }
+static_assert(chunks_of(INT32_MAX, 256, 64) == 64, "a table's longest row");
 
 }  // namespace
 

@@ -341,3 +341,39 @@ def test_tokens_of_a_fork_whose_pages_are_gone_stay_hidden():
     torch.cuda.synchronize()
     assert not y[:8].any()                                         # they see nothing, themselves among it
     assert torch.equal(y[8:], x[8:, :H])                           # ones, in codes of 127 and a scale of 1 / 127
+
+
+def test_the_widest_table():
+    """One row of as many entries as a table may have: ranges at its end, lists of padding, pages that move."""
+    torch = torch_cuda()
+    stride, n = (1 << 31) - 1, 64
+    table = torch.full((1, stride), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(n, dtype=torch.int32, device="cuda")
+    places = torch.tensor([0, 5, 1 << 27, stride - 20000, stride - 16384, stride - 300, stride - 1], device="cuda")
+    pages_of = torch.tensor([50, 3, 60, 7, 20, 33, 63], dtype=torch.int32, device="cuda")
+    table[0, places] = pages_of
+    refs[pages_of.long()] = 1
+    book = qlin.Kv8Book(refs, table, 16)
+    say("kv8 pages: a row of 2^31 - 1 entries: fork of padding")
+    m = up(np.full((2, 2), 77))
+    qlin.qlin_kv8_fork(book, up([-1]), up([0]), up([5]), m)
+    torch.cuda.synchronize()
+    assert m.tolist() == [[1, 0], [-1, -1]] and int((refs == 1).sum()) == 7
+    say("free of what lies behind 2^31 - 17 tokens")
+    qlin.qlin_kv8_free(book, up([0]), up([(1 << 31) - 17]))
+    torch.cuda.synchronize()
+    assert table[0, places].tolist() == [50, 3] + [-1] * 5 and refs.nonzero().flatten().tolist() == [3, 50]
+    table[0, places] = pages_of
+    refs[pages_of.long()] = 1
+    say("free up to 2^31 - 1 tokens, a range that ends before the row does")
+    qlin.qlin_kv8_free(book, up([0]), None, up([(1 << 31) - 1]))
+    torch.cuda.synchronize()
+    assert table[0, places].tolist() == [-1, -1] + pages_of.tolist()[2:] and int((refs == 1).sum()) == 5
+    say("compact and the rest")
+    m = up(np.full((1 + 32, 2), 77))
+    qlin.qlin_kv8_compact(book, m)
+    torch.cuda.synchronize()
+    assert table[0, places].tolist() == [-1, -1, 1, 4, 3, 2, 0] and m[0].tolist() == [5, 0]
+    qlin.qlin_kv8_free(book, up([0]))
+    torch.cuda.synchronize()
+    assert not refs.any() and int(table.amax()) == -1
