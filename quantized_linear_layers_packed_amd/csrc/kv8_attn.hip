@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
       load_rows<D, BF16>(a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(h) * D, g, qf[n], &cq[n]);
       cq[n] *= a.scale;
       pos[n] = seq.start + t;
-      low[n] = a.window > 0 ? max(pos[n], 0) - a.window + 1 : 0;
+      low[n] = window_start(pos[n], a.window);
       if constexpr (SCORED) {
         start[n] = a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0;
         last[n] = sight.last(pos[n]);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[n][d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const int low_most = a.window > 0 ? max(p1, 0) - a.window + 1 : 0;
+    const int low_most = window_start(p1, a.window);
 
     // Loads of a tile: the pages of this lane's K rows (tokens 16 ((lane / 4) % 4) + ..)
     // and V rows (tokens 16 g ..).

@@ -107,6 +107,10 @@ struct Kv8Sight {
   __device__ __forceinline__ int last(int pos) const { return pos < 0 ? -1 : max(pos, prefix - 1); }
 };
 
+// First position of the window of the query at pos, never below 0: a window may be as
+// wide as int, and positions are subtracted from what comes out.
+__device__ __forceinline__ int window_start(int pos, int window) { return window > 0 ? max(max(pos, 0) - window + 1, 0) : 0; }
+
 // The tiles of 64 positions that the rows at positions p0 .. p1 see: those of the
 // first tokens and those from the start of the window of p0.
 struct Kv8Tiles {
@@ -116,7 +120,7 @@ struct Kv8Tiles {
       sinks = first = count = 0;
       return;
     }
-    first = window > 0 ? max(0, max(p0, 0) - window + 1) / kTile : 0;
+    first = window_start(p0, window) / kTile;
     sinks = min(sink_tokens > 0 ? (sink_tokens - 1) / kTile + 1 : 0, first);
     count = sinks + p1 / kTile - first + 1;
   }
@@ -125,7 +129,7 @@ struct Kv8Tiles {
     const int last = sight.last(p1);
     const bool any = p1 >= 0 && sight.start0 <= last;
     from = sight.start0 / kTile;
-    first = max(window > 0 ? max(0, max(p0, 0) - window + 1) : 0, sight.start0) / kTile;
+    first = max(window_start(p0, window), sight.start0) / kTile;
     sinks = any && sink_tokens > 0 ? max(min((sight.kept1 - 1) / kTile + 1, first) - from, 0) : 0;
     count = any ? sinks + last / kTile - first + 1 : 0;
   }

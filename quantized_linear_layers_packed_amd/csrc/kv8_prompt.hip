@@ -140,7 +140,7 @@ __device__ __forceinline__ int nth_row_tile(const Kv8AttnArgs& a, const Kv8Seq& 
   const auto tiles_of = [&](int row_tile) {
     const int r0 = max(row_tile, 0) * ROWS, first = min(r0, rows - 1), t0 = a.by_group(first);
     const int p1 = seq.start + a.by_group(min(first + ROWS, rows) - 1);
-    const int low = a.window > 0 ? max(seq.start + t0, 0) - a.window + 1 : 0, start = min(max(a.starts[seq.row + t0], 0), seq.len);
+    const int low = window_start(seq.start + t0, a.window), start = min(max(a.starts[seq.row + t0], 0), seq.len);
     return r0 < rows ? max(p1, prefix - 1) / kTile - max(low, start) / kTile + 1 : 0;
   };
   const int last = a.row_tiles - 1 - (lane << shift);
@@ -197,8 +197,8 @@ __global__ __launch_bounds__(64 * W, kPromptOccupancy<D>) void kv8_prompt_kernel
     // this lane's row
     const int r = r0 + min(32 * wv + ql, nrows - 1), t = a.by_group(r), hq = head * G + r - t * G;
     const bool mine = 32 * wv + ql < nrows;
-    const int pos = seq.start + t, low = a.window > 0 ? max(pos, 0) - a.window + 1 : 0;
-    const int low_most = a.window > 0 ? max(p1, 0) - a.window + 1 : 0;
+    const int pos = seq.start + t, low = window_start(pos, a.window);
+    const int low_most = window_start(p1, a.window);
     // (with other scores) this row sees start .. last, its first tokens end at `kept`; its slope times -log2(e)
     const int start = FORM && a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0, last = FORM ? rt.sight.last(pos) : 0;
     const int kept = FORM ? start + min(a.sinks, seq.len - start) : 0;
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
     // this lane's row
     const int r = r0 + min(16 * wv + ql, nrows - 1), t = a.by_group(r), hq = head * G + r - t * G;
     const int pos = seq.start + t;
-    const int low_most = a.window > 0 ? max(rt.p1, 0) - a.window + 1 : 0;
+    const int low_most = window_start(rt.p1, a.window);
     const int start = a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0;
     const float slope = a.slopes ? a.slopes[hq] * -1.44269504088896340736f : 0.0f;
     h8_t qf[KU][2];
@@ -621,7 +621,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
             for (int i = 0; i < 4; ++i) st[T][i] = fmaf(slope, fabsf(away + static_cast<float>(4 * T + i)), st[T][i]);
         }
         if (!full) {
-          const uint32_t seen = sight_bits<16>(base + 16 * g, start, rt.sight.last(pos), a.window > 0 ? max(pos, 0) - a.window + 1 : 0,
+          const uint32_t seen = sight_bits<16>(base + 16 * g, start, rt.sight.last(pos), window_start(pos, a.window),
                                                start + min(a.sinks, seq.len - start), (held >> g) & 1u);
           iv = seen != 0 ? iv : 0.0f;                         // scales of hidden pages may be anything, NaN among it
 #pragma unroll

@@ -457,3 +457,14 @@ def test_two_streams_at_once():
         assert all(torch.equal(x, y) for x, y in zip(result(m)[2:3] + result(m)[4:], got[2:3] + got[4:]))
         table, refs = m["b"].d_table.cpu().numpy(), m["b"].d_refs.cpu().numpy()
         assert np.array_equal(np.bincount(table[table >= 0], minlength=500), refs) and int(m["grown"][0, 1]) == 0
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 400, 1 << 30])
+@pytest.mark.parametrize("D,new,max_kv", [(64, 1, None), (128, 12, None), (128, 90, None), (128, 90, 64), (256, 90, 64)])
+def test_windows_as_wide_as_int(D, new, max_kv, window):
+    """A prefix behind the queries stays visible in them, in every kernel."""
+    s = Setup(57, D, 16, 1, [new, new], [600, new], max_kv=max_kv)
+    kw = dict(Q=3.0 * s.rng.standard_normal((s.T, 4, D)), prefix=[600, new], starts=documents(s, 300), cap=20.0)
+    wide = back(check_scored(s, 4, F16, window=window, **kw))
+    assert np.array_equal(back(run_scored(s, 4, F16, window=window, sinks=5, **kw)[0]), wide)
+    check_scored(s, 4, F16, window=window, sinks=(1 << 31) - 1, **kw)
