@@ -118,7 +118,7 @@ __global__ __launch_bounds__(64 * W, row_occupancy(D, NT)) void kv8_rows_kernel(
         start[n] = a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0;
         last[n] = sight.last(pos[n]);
         kept[n] = start[n] + min(a.sinks, seq.len - start[n]);
-        slope[n] = a.slopes ? a.slopes[h] * -1.44269504088896340736f : 0.0f;
+        slope[n] = a.slopes ? bias_slope(a.slopes[h]) : 0.0f;
       }
       m[n] = kNone;
       l[n] = 0.0f;

@@ -161,6 +161,12 @@ __device__ __forceinline__ float capped(float z, float cap, float add) {
   return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.0f), cap + add);
 }
 
+// A slope of the bias in the exponent of two, kept finite: what is 0 away then counts as
+// it is, whatever the slope.
+__device__ __forceinline__ float bias_slope(float slope) {
+  return fmaxf(fminf(slope * -1.44269504088896340736f, 3.40282347e38f), -3.40282347e38f);
+}
+
 // The sequence with the n-th most tiles (n from 0, ties to the lower index), found
 // by every wave for itself: a search down the bits of (tiles, 255 - index), a few
 // scalar instructions a bit.  Workgroups that start in this order end together:

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * W, kPromptOccupancy<D>) void kv8_prompt_kernel
     // (with other scores) this row sees start .. last, its first tokens end at `kept`; its slope times -log2(e)
     const int start = FORM && a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0, last = FORM ? rt.sight.last(pos) : 0;
     const int kept = FORM ? start + min(a.sinks, seq.len - start) : 0;
-    const float slope = FORM && a.slopes ? a.slopes[hq] * -1.44269504088896340736f : 0.0f;
+    const float slope = FORM && a.slopes ? bias_slope(a.slopes[hq]) : 0.0f;
     h8_t qf[KS];                                            // slice s: dimensions 16 s + 8 h .. + 7
     float cq = a.scale;
     {
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(64 * kThinWaves, 2) void kv8_thin_kernel(const Kv8A
     const int pos = seq.start + t;
     const int low_most = window_start(rt.p1, a.window);
     const int start = a.starts ? min(max(a.starts[seq.row + t], 0), seq.len) : 0;
-    const float slope = a.slopes ? a.slopes[hq] * -1.44269504088896340736f : 0.0f;
+    const float slope = a.slopes ? bias_slope(a.slopes[hq]) : 0.0f;
     h8_t qf[KU][2];
     float cq;
     load_rows<D, BF16>(a.Q + static_cast<size_t>(seq.row + t) * a.q_stride + static_cast<size_t>(hq) * D, g, qf, &cq);

@@ -468,3 +468,16 @@ def test_windows_as_wide_as_int(D, new, max_kv, window):
     wide = back(check_scored(s, 4, F16, window=window, **kw))
     assert np.array_equal(back(run_scored(s, 4, F16, window=window, sinks=5, **kw)[0]), wide)
     check_scored(s, 4, F16, window=window, sinks=(1 << 31) - 1, **kw)
+
+
+@pytest.mark.parametrize("slope", [2.3e38, 2.4e38, 3.4028234e38])
+@pytest.mark.parametrize("D,new,max_kv", [(64, 1, None), (128, 90, None), (128, 90, 64), (256, 90, 64)])
+def test_slopes_up_to_the_largest_float(D, new, max_kv, slope):
+    """Beside such a slope a query sees its own position alone: its value, off by the roundings of the weight (2^-11) and of
+    the output (2^-11) and a few of fp32."""
+    s = Setup(58, D, 16, 1, [new, new], [600, new], max_kv=max_kv)
+    Y = back(run_scored(s, 4, F16, slopes=np.full(4, slope, F))[0])
+    for b, m in enumerate(s.kv):
+        _, v, _ = okv.values(s.k, s.v, s.scales, s.table[b], m, 0)
+        own = v[m - new:, None]
+        assert (np.abs(Y[new * b:new * b + new] - own) <= (2.0 ** -10 + 2.0 ** -18) * np.abs(own)).all()
