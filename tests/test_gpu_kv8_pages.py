@@ -377,3 +377,20 @@ def test_the_widest_table():
     qlin.qlin_kv8_free(book, up([0]))
     torch.cuda.synchronize()
     assert not refs.any() and int(table.amax()) == -1
+
+
+@pytest.mark.parametrize("num_pages,count", [(16380, 4095), (16384, 4096), (16388, 4097), (32772, 8193), (70000, 17500)])
+def test_compactions_of_many_pages(num_pages, count):
+    """Every other page in use: a quarter of the pool moves, more than LDS holds sources of at once.  The table looks its
+    entries up in all of the moves or in some of them; also a small one, beside pages that are held outside of it."""
+    r = np.random.default_rng(num_pages)
+    used = np.arange(1, num_pages, 2)
+    for rows, stride in ((5, 9000), (3, 300)):
+        for most in (num_pages // 2, count, count - 1, 4100):
+            b = Book(num_pages, rows, stride)
+            flat = b.table.reshape(-1)
+            n = min(len(flat), len(used))
+            flat[r.permutation(len(flat))[:n]] = r.permutation(used)[:n]
+            b.refs[used] = 1
+            b.upload()
+            assert b.compact(most) == (min(count, most), 0)

@@ -481,3 +481,35 @@ def test_slopes_up_to_the_largest_float(D, new, max_kv, slope):
         _, v, _ = okv.values(s.k, s.v, s.scales, s.table[b], m, 0)
         own = v[m - new:, None]
         assert (np.abs(Y[new * b:new * b + new] - own) <= (2.0 ** -10 + 2.0 ** -18) * np.abs(own)).all()
+
+
+@pytest.mark.parametrize("dtype,D,G,Hk,new", [(F16, 128, 16, 2, 1100),       # 138 row tiles: 34 groups of four and two
+                                              (BF16, 128, 16, 1, 2070),      # 259: 32 of eight and three
+                                              (F16, 256, 16, 1, 2070), (F16, 64, 16, 2, 1040)])
+def test_long_documents_first_of_many_row_tiles(dtype, D, G, Hk, new):
+    s = Setup(59, D, 64, Hk, [new], [new], max_kv=64)
+    r = np.random.default_rng(60)
+    Q = 3.0 * r.standard_normal((s.T, Hk * G, D))
+    wild = r.integers(-100, new + 100, s.T).astype(np.int32)
+    for kw in (dict(starts=documents(s, 333), cap=20.0), dict(starts=wild, prefix=[new // 2], window=200, sinks=9)):
+        first = back(check_scored(s, G, dtype, Q=Q, **kw))
+        assert np.array_equal(back(run_scored(s, G, dtype, Q=Q, **kw)[0]), first)
+
+
+def test_packed_documents_of_whole_pages_equal_sequences_of_their_own():
+    lens = [128, 64, 192, 64, 256]
+    s = Setup(38, 128, 64, 2, [sum(lens)], [sum(lens)])
+    Q = s.rng.standard_normal((s.T, 8, 128))
+    at = np.cumsum([0] + lens)
+    packed = back(check_scored(s, 4, F16, Q=Q, starts=np.repeat(at[:-1], lens).astype(np.int32)))
+    for a, n in zip(at[:-1], lens):
+        t = Setup(38, 128, 64, 2, [sum(lens)], [sum(lens)])
+        t.table = s.table[:, a // 64:].copy()
+        t.new, t.kv = [n], [n]
+        t.offsets, t.kv_lens, t.T = np.array([0, n], np.int32), np.array([n], np.int32), n
+        t.counts = (n, n)
+        t.upload()
+        Y, Qr, scale = run_attention(t, 4, F16, Q=Q[a:a + n])
+        ref, A, score, peak = okv.attention(t.k, t.v, t.scales, t.offsets, t.kv_lens, t.table, Qr, float(F(scale)), 0, 0)
+        tol = attention_bound(A, ref, score, peak, 128, n, F16) + scored_bound(A, ref, score, peak, 0 * score, 128, sum(lens), F16, 0.0)
+        assert (np.abs(back(Y).astype(np.float64) - packed[a:a + n]) <= tol).all()
