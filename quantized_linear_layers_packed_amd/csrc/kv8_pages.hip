@@ -38,7 +38,9 @@ constexpr int kStep = kThreads * kEach;
 __device__ __forceinline__ bool is_page(int page, int pages) { return static_cast<unsigned>(page) < static_cast<unsigned>(pages); }
 // An entry that grow looks for pages behind: held, or its tokens came with a fork and their
 // page was gone by then.  Pages dealt out for such tokens would show what others left there.
-__device__ __forceinline__ bool is_past(int page, int pages) { return is_page(page, pages) || page == kKv8Gone; }
+// (A selection: as two comparisons or-ed the searches spill scalar registers, and the grow of
+// 32768 pages takes 25.2 instead of 24.2 us.)
+__device__ __forceinline__ bool is_past(int page, int pages) { return is_page(page == kKv8Gone ? 0 : page, pages); }
 
 // Sum of v over the threads before this one, and over all in *total.
 // part: 16 ints in LDS, free again when the call returns.
