@@ -154,7 +154,7 @@ void kv8_attn_launch(Kv8AttnPlan p, int* counters, char* partials, int dtype, hi
 // The kernel for many rows: rows of a workgroup, workgroups that share a compute
 // unit, bytes of a split's partial result; and for documents, where row tiles are not
 // split, waves of a workgroup (of 32 rows each).
-int kv8_prompt_document_waves(int dim);
+int kv8_prompt_document_waves();
 int kv8_prompt_rows(int dim);
 int kv8_prompt_resident(int dim);
 size_t kv8_prompt_partial(int dim);

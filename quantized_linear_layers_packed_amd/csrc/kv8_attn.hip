@@ -458,7 +458,7 @@ size_t plan_splits(Kv8AttnArgs* a, int nt, long long rows, int cus) {
 // smaller ones, which need no workspace either, and those with the most tiles begin first.
 size_t plan_launch(Kv8AttnArgs* a, int nt, long long rows, int cus) {
   const size_t bytes = plan_splits(a, nt, rows, cus);
-  const int waves = kv8_prompt_document_waves(a->c.dim);
+  const int waves = kv8_prompt_document_waves();
   if (!nt && a->starts && a->splits == 1 && 32 * waves < kv8_prompt_rows(a->c.dim)) {
     const long long most = std::max<long long>(1, (1LL << 22) / (static_cast<long long>(a->c.seqs) * a->c.heads));
     a->waves = waves;

@@ -797,7 +797,7 @@ void prompt_launch(const Kv8AttnArgs& a, int dtype, hipStream_t stream) {
 
 }  // namespace
 
-int kv8_prompt_document_waves(int dim) { return dim == 128 ? kDocumentWaves : 4; }
+int kv8_prompt_document_waves() { return kDocumentWaves; }
 
 int kv8_prompt_rows(int dim) { return 32 * (dim == 64 ? kPromptWaves<64> : dim == 128 ? kPromptWaves<128> : kPromptWaves<256>); }
 
