@@ -535,7 +535,8 @@ qlin_status qlin_kv8_fork(const qlin_kv8_book* book, const int32_t* parents, con
  * end[i]-1 (NULL: from 0 on, to the table's end): whole sequences, pages behind a
  * window, pages of rejected drafts.  A page is free once nothing holds it.  Rows
  * outside the table are skipped, rows may be named more than once.  Lists: device
- * int32 [count], count <= 65535. */
+ * int32 [count], count <= 65535.  A row that keeps the page in which it is cut back shares
+ * it still, if it did (see qlin_kv8_fork); one that keeps none is a new one to grow. */
 qlin_status qlin_kv8_free(const qlin_kv8_book* book, const int32_t* rows, const int32_t* begin, const int32_t* end,
                           int count, hipStream_t stream);
 

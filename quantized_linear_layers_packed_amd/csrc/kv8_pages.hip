@@ -9,17 +9,20 @@
 //
 // A choice over the whole pool (the r-th free page) is a prefix sum over refs.  One
 // workgroup of 1024 threads makes it, 16 pages to a thread and 16384 to a step, and
-// stops at the last page that it needs: a pool that fills the card's memory has some
-// ten thousand pages, so its counts are a few hundred KB, and what bounds these
-// kernels is the latency of dependent loads and barriers, which a second launch
-// would only add to.  What touches a whole table is spread over the device.
+// stops at the last page that it needs.  A pool that fills the card's memory has from
+// some ten thousand pages on (of 128 tokens in many layers) to a few hundred thousand:
+// 40 KB to a few MB of counts, and what bounds these kernels is the latency of
+// dependent loads and barriers, which a second launch would only add to.  What touches
+// a whole table is spread over the device.
 //
 // Measured, calls and all: a token for each of 256 sequences (131072 pages; two
 // releases and the grow) 15.6 us, of which the host's three calls are 14; 32768 pages
-// for 16 prompts 28.5 us (the grow 23: one workgroup's 65536 stores, and the search for
-// the rows' ends), 16168 for 512 prompts of 32 pages 58; 128 forks of two prompts with a page of 131 KB each to copy in 4 layers
-// 39 us, the copies 17; a pool of 6082 pages half in use, 1520 of 262 KB moved in 2 layers,
-// 168 us, 4.75 TB/s (a large copy: 4.74).
+// for 16 prompts 29.5 us (the grow 24: one workgroup's 65536 stores, and the search for
+// the rows' ends), 16168 for 512 prompts of 32 pages 59; 128 forks of two prompts with a
+// page of 131 KB each to copy in 4 layers 39 us, the copies 17; a pool of 6082 pages half
+// in use, 1520 of 262 KB moved in 2 layers, 168 us, 4.74 TB/s (a large copy: 4.73).
+// The grow of a token for each of 256 sequences takes 7 us where free pages lie among the
+// first 16384 of the pool and 24 behind 98204 pages in use, whose counts are read twice.
 
 #include <algorithm>
 
@@ -164,7 +167,7 @@ __device__ __forceinline__ int entries_of(int len, const Kv8Book& k) {
 // Needs of the rows that have more to find: searched back from the end for the last
 // held (or gone) entry, ROWS rows of a wave and 1024 / ROWS entries of each at a time.  With one, few
 // long rows are found soonest (16 of 2500 entries: 4 reads in turn), with four, many short
-// ones (512 prompts of 32 pages 89 -> 58 us).
+// ones (512 prompts of 32 pages, releases and all, 103 -> 59 us; 16 of 2500 30.6 with either).
 constexpr int kAFew = 2 * kThreads / 64;
 template <int ROWS>
 __device__ __forceinline__ void search_rows(const Kv8Book& k, const int32_t* lens, int* need) {

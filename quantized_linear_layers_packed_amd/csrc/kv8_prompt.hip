@@ -94,9 +94,10 @@ __device__ __forceinline__ void lookahead() {
 constexpr int kPlain = 0, kScored = 1, kCapped = 2;
 // Waves of a workgroup for documents, whose row tiles see a few tiles each, where they
 // are not split.  Heads of 128: with 4, two workgroups share a compute unit, and one's
-// beginning (lengths, starts, pages, codes in turn) hides behind the other's products:
-// documents of 745 tokens on average 141 -> 133 us.  Prompts without documents are as
-// fast with 8 or up to 2 % faster.
+// beginning (lengths, starts, pages, codes in turn) hides behind the other's products.
+// 8191 tokens with 8 and with 4: documents of 745 on average 126 and 125 us with 32 / 8
+// heads, 91 and 72 with 16 / 16; of 137 75 and 71; a single one 595 and 617, as for
+// prompts without documents, which keep 8.
 constexpr int kDocumentWaves = 4;
 // Waves of a workgroup of the kernel with 16 rows to a wave.
 constexpr int kThinWaves = 8;
@@ -128,9 +129,10 @@ struct RowTile {
 // 2^shift row tiles, each as long as the longer of its last and its first (which may end
 // the document before), are searched down the bits of their tiles (up to 255; more tie).
 // What is left of the first row tiles comes last.
-// 8191 tokens of documents of 745 on average 139 -> 131 us with 32 / 8 heads, 85 -> 65 with
-// 16 / 16, 16384 tokens of nine documents 215 -> 200; but of 137 tokens 63 -> 68: the search is a
-// microsecond of a workgroup's beginning, and the host does not know the documents.
+// 8191 tokens of documents of 745 on average 128 -> 125 us with 32 / 8 heads, 92 -> 72 with
+// 16 / 16, 16384 tokens of nine documents with 16 / 4 214 -> 202; but of 137 tokens 67 -> 71:
+// the search is a microsecond of a workgroup's beginning, and the host does not know the
+// documents.
 template <int ROWS>
 __device__ __forceinline__ int nth_row_tile(const Kv8AttnArgs& a, const Kv8Seq& seq, int b, int rows, int n) {
   const int shift = a.row_tiles > 64 ? 26 - __builtin_clz(a.row_tiles - 1) : 0, groups = a.row_tiles >> shift;
@@ -464,7 +466,7 @@ __global__ __launch_bounds__(64 * W, kPromptOccupancy<D>) void kv8_prompt_kernel
 
 // The same for whole row tiles of heads of 256 with other scores, on the 16x16x32
 // instruction: a wave holds 16 rows, so that two of them share a SIMD, whose vector
-// unit a single wave fills half: ragged prefix prompts 488 -> 354 us.  S^T and P lie as in
+// unit a single wave fills half: ragged prefix prompts 489 -> 317 us.  S^T and P lie as in
 // the kernel for few rows (kv8_attn.hip): lane (q, g) gets the weights of row q and the
 // run of tokens 16 g .. 16 g + 15, and one pair of scales.  K's rows lie in LDS in the
 // order in which the products take them (row 16 t + r: token 16 (r / 4) + 4 t + r % 4).
@@ -473,10 +475,14 @@ __global__ __launch_bounds__(64 * W, kPromptOccupancy<D>) void kv8_prompt_kernel
 // products.  The 16 bytes of lane (r, g) of an operand lie in a plane for each g, a
 // multiple of all the banks apart, and swizzled by r so that 16 rows fill every bank
 // once, whichever g's the lanes that are served together belong to; a g's own constants
-// keep the planes' swizzles apart for the writes: 354 -> 317 us (padded rows: a third of
-// the time bank conflicts).  What is left is vector (62 % of the cycles) and matrix
+// keep the planes' swizzles apart for the writes (with padded rows, a third of the time
+// bank conflicts, 354 us).  What is left is vector (62 % of the cycles) and matrix
 // instructions (32 %).  Heads of 128 this way, four waves to a SIMD, are slower than with
 // 32 rows to a wave (a capped prompt of 8192 1449 -> 1678 us).
+// Row tiles in splits, which this kernel has no partial results for, are faster in splits
+// than whole here: 512 tokens after 7680 cached ones, 16 / 4 heads, 150 against 301 us,
+// 4 x 256 after 8192 273 and 311, 1024 after 8192 293 and 337.  The plain attention has no
+// form of it.
 template <int D>
 struct alignas(16) ThinTile {
   h8_t k[4][kTile][D / 32];                                 // [g][row][slice (u, e) ^ thin_k(row, g)]
